@@ -86,7 +86,9 @@ typedef enum {
                                   unspecified */
 #define LSA_DEV_BAD_VALUE 0x40 /* lsa_attend_si: a V element of magnitude >= 65520 (or not
                                   finite) in a sink or window run, which that call multiplies
-                                  in fp16; the outputs of the rows that read it are unspecified */
+                                  in fp16; the outputs of the rows that read it are unspecified.
+                                  lsa_store_fp4: a K or V element that is not finite (its group
+                                  of 16 is stored as NaN) */
 
 /* Selection budget. sink + window + topk is the index-set length ("budget").
  * hi_block == 0 switches HI off; otherwise blocks of hi_block tokens aligned
@@ -117,6 +119,26 @@ typedef struct {
     const int32_t *q_seq;     /* device [n_q]: sequence of each query row */
     const int32_t *q_len;     /* device [n_q]: visible length of each query row */
 } lsa_batch_t;
+
+/* The newest rows of packed sequences of different lengths: whole prompts,
+ * chunks of prompts, or one new token each. Sequence b holds seq_lens[b]
+ * tokens, its newest n = row_offset[b+1] - row_offset[b] ones are the rows
+ * row_offset[b] .. row_offset[b+1] - 1, and row i of them is token
+ * seq_lens[b] - n + i, which sees the seq_lens[b] - n + i + 1 tokens up to
+ * itself. A sequence may have no rows; one with more rows than tokens, or
+ * whose rows or tokens lie outside the buffers, sets LSA_DEV_BAD_LENGTH and is
+ * skipped: its outputs are left as they were, as are rows of no sequence. */
+typedef struct {
+    int32_t n_seq;            /* number of sequences, >= 1 */
+    int32_t n_rows;           /* rows in all (bounds every row access), >= 0 */
+    int32_t max_len;          /* host-side upper bound on every seq_lens */
+    int32_t reserved;         /* must be 0 */
+    int64_t total_tokens;     /* rows in the packed caches (bounds every access) */
+    const int32_t *row_offset;/* device [n_seq + 1]: first row of each sequence,
+                                 ascending, and the end of the last */
+    const int64_t *kv_offset; /* device [n_seq]: first cache row of each sequence */
+    const int32_t *seq_lens;  /* device [n_seq]: tokens present in each sequence */
+} lsa_prompts_t;
 
 /* Largest sizes the kernels are compiled for. */
 #define LSA_MAX_HEADS_I 64    /* H_I */
@@ -382,6 +404,77 @@ lsa_status_t lsa_attend(const uint16_t *const *q, const uint16_t *const *k_cache
  */
 lsa_status_t lsa_attend_fp8(const uint16_t *const *q, const uint8_t *const *k_cache,
                             const uint8_t *const *v_cache, const float *k_scale,
+                            const float *v_scale, int32_t H_q, int32_t H_kv, int32_t d,
+                            const int32_t *index_sets, int32_t budget,
+                            const lsa_batch_t *batch, int32_t layers_per_index,
+                            float *const *out, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, void *stream);
+
+/* ----------------------------------------------------------------------- */
+/* 4-bit K/V caches                                                          */
+/* ----------------------------------------------------------------------- */
+/* The pages name low-precision KV caches without a format (see
+ * lsa_attend_fp8); this one holds a K or V number in 4.5 bits. One (token, kv
+ * head) row of 128 channels is
+ *    codes   uint8 [64]: OCP E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *            negatives), channel 2 i in the low half of byte i, 2 i + 1 in the high;
+ *    groups  uint8 [8]: an OCP E4M3 scale for each 16 channels;
+ * and, with one scale per layer for K and one for V,
+ *    number = layer scale * E4M3(groups[c / 16]) * E2M1(code c).
+ *
+ * lsa_store_fp4 writes new K and V rows into such caches: any number of
+ * newest tokens of each sequence (see lsa_prompts_t), one in a decode step, a
+ * whole prompt at once. For each group of 16 numbers x and the layer's scale S
+ *    E4M3(scale) = max|x| / (6 S)  to nearest, ties to even, at most 448
+ *    E2M1(code)  = x / (E4M3(scale) S)  to nearest, ties to even, at most 6
+ * both rounded from the exact quotient; a scale of 0 has codes 0. A group
+ * with an element that is not finite gets the scale NaN and codes 0 (and sets
+ * LSA_DEV_BAD_VALUE).
+ *
+ * k_new, v_new  host [layers] arrays of device bf16 [n_rows] rows of H_kv * d
+ *               elements, k_stride and v_stride elements from one row to the
+ *               next (H_kv * d when contiguous; more for a view of a fused
+ *               projection; a multiple of 8).
+ * k, v          host [layers] arrays of device uint8 [total_tokens][H_kv][d/2].
+ * k_group, v_group host [layers] arrays of device uint8 [total_tokens][H_kv][d/16].
+ * k_scale, v_scale host [layers] arrays of layer scales: powers of two in
+ *               [2^-100, 2^100], which only place E4M3's range (for numbers of
+ *               size m, m / 8 is a good one).
+ * k_round, v_round host [layers] arrays of device bf16 [n_rows][H_kv][d], both
+ *               or NULL: the numbers that the cache now holds for the new rows
+ *               (exact where they are bf16 normals), for attending a prompt over
+ *               the same values that decoding will read.
+ * Rows of two sequences that share cache rows race. All device pointers
+ * 16-byte aligned (the group scales 8). Supported: d == 128; 1 <= H_kv <= 256;
+ * 1 <= layers <= LSA_MAX_LAYERS; n_rows * H_kv < 2^31. One launch.
+ */
+lsa_status_t lsa_store_fp4(const uint16_t *const *k_new, int64_t k_stride,
+                           const uint16_t *const *v_new, int64_t v_stride,
+                           int32_t H_kv, int32_t d, const lsa_prompts_t *prompts,
+                           int32_t layers, const float *k_scale, const float *v_scale,
+                           uint8_t *const *k, uint8_t *const *k_group,
+                           uint8_t *const *v, uint8_t *const *v_group,
+                           uint16_t *const *k_round, uint16_t *const *v_round,
+                           int32_t *dev_status, void *stream);
+
+/* lsa_attend over a 4-bit cache, the numbers as above. The set, the softmax,
+ * the GQA mapping, the output and the device-side errors are lsa_attend's;
+ * every entry of a set that is not -1 counts, wherever it stands. A query row
+ * that is not finite gives NaN, as does an entry whose K row holds a NaN.
+ *
+ * k_scale, v_scale  host [G] arrays of finite floats (any, not only the powers
+ *                   of two that lsa_store_fp4 writes).
+ * workspace         lsa_attend_fp4_workspace_size() bytes (split partials; no
+ *                   initialisation needed; may be NULL when that is 0).
+ * Supported: as lsa_attend. One launch, plus a split merge with several splits.
+ */
+size_t lsa_attend_fp4_workspace_size(const lsa_batch_t *batch, int32_t H_q, int32_t H_kv, int32_t d,
+                                     int32_t budget, int32_t layers_per_index);
+int32_t lsa_attend_fp4_launches(const lsa_batch_t *batch, int32_t H_q, int32_t H_kv, int32_t d,
+                                int32_t budget, int32_t layers_per_index);
+lsa_status_t lsa_attend_fp4(const uint16_t *const *q, const uint8_t *const *k,
+                            const uint8_t *const *k_group, const uint8_t *const *v,
+                            const uint8_t *const *v_group, const float *k_scale,
                             const float *v_scale, int32_t H_q, int32_t H_kv, int32_t d,
                             const int32_t *index_sets, int32_t budget,
                             const lsa_batch_t *batch, int32_t layers_per_index,

@@ -32,7 +32,8 @@ EXPORTS = ["lsa_version", "lsa_last_cuda_error", "lsa_status_string", "lsa_hi_bl
            "lsa_merge_pairs", "lsa_score_tokens", "lsa_score_blocks", "lsa_attend_lse", "lsa_shard_sets",
            "lsa_combine", "lsa_attend_grouped_workspace_size", "lsa_attend_grouped_launches", "lsa_attend_grouped",
            "lsa_attend_si_workspace_size", "lsa_attend_si_launches", "lsa_attend_si",
-           "lsa_attend_noalloc", "lsa_append_index", "lsa_append_index_launches"]
+           "lsa_attend_noalloc", "lsa_append_index", "lsa_append_index_launches", "lsa_store_fp4",
+           "lsa_attend_fp4_workspace_size", "lsa_attend_fp4_launches", "lsa_attend_fp4"]
 
 MERGE_ID_BITS = 24  # LSA_MERGE_ID_BITS
 
@@ -57,6 +58,12 @@ class _Batch(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("total_tokens", ctypes.c_int64),
                 ("kv_offset", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("blk_offset", ctypes.c_void_p),
                 ("q_seq", ctypes.c_void_p), ("q_len", ctypes.c_void_p)]
+
+
+class _Prompts(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("total_tokens", ctypes.c_int64),
+                ("row_offset", ctypes.c_void_p), ("kv_offset", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
 
 
 @dataclass
@@ -97,6 +104,30 @@ class Batch:
                       int(self.total_tokens), self.kv_offset.data_ptr(), self.seq_lens.data_ptr(),
                       self.blk_offset.data_ptr() if self.blk_offset is not None else None,
                       self.q_seq.data_ptr(), self.q_len.data_ptr())
+
+
+@dataclass
+class Prompts:
+    """The newest rows of packed sequences of different lengths (include/lsa.h, lsa_prompts_t); tensors live on
+    the device that runs the call. row_offset is ascending: sequence b's rows are row_offset[b] ..
+    row_offset[b + 1] - 1, its newest tokens."""
+    row_offset: torch.Tensor  # int32 [n_seq + 1]
+    kv_offset: torch.Tensor   # int64 [n_seq]
+    seq_lens: torch.Tensor    # int32 [n_seq]
+    n_rows: int
+    max_len: int
+    total_tokens: int
+
+    def c(self) -> _Prompts:
+        ro, ko, sl = self.row_offset, self.kv_offset, self.seq_lens
+        if (ro.dtype is not torch.int32 or ko.dtype is not torch.int64 or sl.dtype is not torch.int32
+                or not (ro.is_contiguous() and ko.is_contiguous() and sl.is_contiguous())):
+            raise TypeError("row_offset and seq_lens must be contiguous int32, kv_offset contiguous int64 tensors")
+        n_seq = sl.numel()
+        if ro.numel() != n_seq + 1 or ko.numel() != n_seq:
+            raise ValueError("row_offset must hold n_seq + 1 values, kv_offset and seq_lens n_seq")
+        return _Prompts(n_seq, self.n_rows, self.max_len, 0, self.total_tokens, ro.data_ptr(), ko.data_ptr(),
+                        sl.data_ptr())
 
 
 _lib = None
@@ -151,6 +182,16 @@ def load_library():
     lib.lsa_attend_fp8.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp),
                                    ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), i32, i32, i32, vp,
                                    i32, ctypes.POINTER(_Batch), i32, ctypes.POINTER(vp), vp, sz, vp, vp]
+    lib.lsa_store_fp4.restype = i32
+    lib.lsa_store_fp4.argtypes = [vp, i64, vp, i64, i32, i32, ctypes.POINTER(_Prompts), i32, vp, vp, vp, vp, vp, vp, vp,
+                                  vp, vp, vp]
+    lib.lsa_attend_fp4_workspace_size.restype = sz
+    lib.lsa_attend_fp4_workspace_size.argtypes = [ctypes.POINTER(_Batch), i32, i32, i32, i32, i32]
+    lib.lsa_attend_fp4_launches.restype = i32
+    lib.lsa_attend_fp4_launches.argtypes = [ctypes.POINTER(_Batch), i32, i32, i32, i32, i32]
+    lib.lsa_attend_fp4.restype = i32
+    lib.lsa_attend_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, ctypes.POINTER(_Batch), i32, vp, vp,
+                                   sz, vp, vp]
     lib.lsa_score_tokens.restype = i32
     lib.lsa_score_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp]
     lib.lsa_score_blocks.restype = i32
@@ -466,6 +507,117 @@ def lsa_attend_noalloc(q: list, k: list, v: list, index_sets: torch.Tensor, batc
     st = lib.lsa_attend_noalloc(qa, ka, va, H_q, H_kv, d, _ptr(index_sets), index_sets.shape[1], ctypes.byref(cb),
                                 G, oa, _ptr(dev_status), _stream(stream))
     _check("lsa_attend_noalloc", st)
+
+
+def _here(t: torch.Tensor) -> None:
+    """Refuse tensors that are not on the device the call would run on."""
+    if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+
+
+def _layers(name: str, ts: list, n: int, dtype: torch.dtype, shape: tuple) -> list:
+    """The device pointers of a per-layer list of contiguous tensors."""
+    if len(ts) != n:
+        raise ValueError(f"{name} must hold one tensor per layer")
+    for t in ts:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise TypeError(f"{name} must hold contiguous {dtype} tensors of shape {shape}")
+    return [t.data_ptr() for t in ts]
+
+
+def _row_stride(name: str, t: torch.Tensor, H: int, d: int) -> int:
+    """Elements from one token to the next of a [tokens, H, d] view whose heads are contiguous."""
+    s = t.stride()
+    if s[2] != 1 or (H > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s[0] if t.shape[0] > 1 else H * d
+
+
+def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_group: list, k_scale: list, v_scale: list,
+                  prompts: Prompts, k_round: list | None = None, v_round: list | None = None,
+                  dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """New K/V rows (lists of G bf16 tensors [n_rows, H_kv, 128]; views whose rows are apart, as of a fused
+    projection, are taken as they are) into 4-bit caches (codes uint8 [T, H_kv, 64], group scales uint8 E4M3
+    [T, H_kv, 8]) with per-layer power-of-two scales. k_round, v_round: the values the caches now hold (bf16
+    [n_rows, H_kv, 128])."""
+    lib = load_library()
+    G = len(k_new)
+    n_rows, H_kv, d = k_new[0].shape
+    T = k[0].shape[0]
+    _here(k_new[0])
+    if n_rows != prompts.n_rows or T < prompts.total_tokens:
+        raise ValueError("k_new must hold prompts.n_rows rows and the caches prompts.total_tokens")
+    strides, ptrs = [], []
+    for name, ts in (("k_new", k_new), ("v_new", v_new)):
+        if len(ts) != G:
+            raise ValueError(f"{name} must hold one tensor per layer")
+        for t in ts:
+            if t.dtype is not torch.bfloat16 or t.shape != (n_rows, H_kv, d):
+                raise TypeError(f"{name} must hold bfloat16 [n_rows, H_kv, d] tensors")
+            strides.append(_row_stride(name, t, H_kv, d))
+            ptrs.append(t.data_ptr())
+        if len(set(strides[-G:])) > 1:
+            raise ValueError(f"{name}: every layer must have the same row stride")
+    u8 = torch.uint8
+    ptrs += _layers("k", k, G, u8, (T, H_kv, d // 2)) + _layers("k_group", k_group, G, u8, (T, H_kv, d // 16))
+    ptrs += _layers("v", v, G, u8, (T, H_kv, d // 2)) + _layers("v_group", v_group, G, u8, (T, H_kv, d // 16))
+    if (k_round is None) != (v_round is None):
+        raise ValueError("k_round and v_round come together")
+    if k_round is not None:
+        ptrs += _layers("k_round", k_round, G, torch.bfloat16, (n_rows, H_kv, d))
+        ptrs += _layers("v_round", v_round, G, torch.bfloat16, (n_rows, H_kv, d))
+    if len(k_scale) != G or len(v_scale) != G:
+        raise ValueError("k_scale and v_scale must hold one scale per layer")
+    buf = (ctypes.c_void_p * len(ptrs))(*ptrs)
+    sc = (ctypes.c_float * (2 * G))(*k_scale, *v_scale)
+    at, step, sa = ctypes.addressof(buf), 8 * G, ctypes.addressof(sc)
+    rounds = (None, None) if k_round is None else (at + 6 * step, at + 7 * step)
+    st = lib.lsa_store_fp4(at, strides[0], at + step, strides[G], H_kv, d, prompts.c(), G, sa, sa + 4 * G, at + 2 * step,
+                           at + 3 * step, at + 4 * step, at + 5 * step, *rounds, _ptr(dev_status), _stream(stream))
+    if st:
+        _check("lsa_store_fp4", st)
+
+
+def lsa_attend_fp4_workspace_size(batch: Batch, H_q: int, H_kv: int, d: int, budget: int, layers: int) -> int:
+    return load_library().lsa_attend_fp4_workspace_size(batch.c(), H_q, H_kv, d, budget, layers)
+
+
+def lsa_attend_fp4_launches(batch: Batch, H_q: int, H_kv: int, d: int, budget: int, layers: int) -> int:
+    """Kernel launches lsa_attend_fp4 issues for this shape."""
+    return load_library().lsa_attend_fp4_launches(batch.c(), H_q, H_kv, d, budget, layers)
+
+
+def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_scale: list, v_scale: list,
+                   index_sets: torch.Tensor, batch: Batch, out: list, workspace: torch.Tensor | None,
+                   dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """lsa_attend over 4-bit K/V caches: codes uint8 [T, H_kv, 64], group scales uint8 E4M3 [T, H_kv, 8], per-layer
+    scales (lists of G tensors and floats)."""
+    lib = load_library()
+    G = len(q)
+    n_q, H_q, d = q[0].shape
+    T, H_kv = k[0].shape[:2]
+    _here(q[0])
+    if index_sets.dtype is not torch.int32 or not index_sets.is_contiguous() or index_sets.shape[0] != n_q:
+        raise TypeError("index_sets must be a contiguous int32 [n_q, budget] tensor")
+    if T < batch.total_tokens:
+        raise ValueError("the caches must hold batch.total_tokens rows")
+    if len(k_scale) != G or len(v_scale) != G:
+        raise ValueError("k_scale and v_scale must hold one scale per layer")
+    u8, rows = torch.uint8, (n_q, H_q, d)
+    ptrs = _layers("q", q, G, torch.bfloat16, rows) + _layers("out", out, G, torch.float32, rows)
+    ptrs += _layers("k", k, G, u8, (T, H_kv, d // 2)) + _layers("k_group", k_group, G, u8, (T, H_kv, d // 16))
+    ptrs += _layers("v", v, G, u8, (T, H_kv, d // 2)) + _layers("v_group", v_group, G, u8, (T, H_kv, d // 16))
+    cb = batch.c()
+    if cb.n_q != n_q:
+        raise ValueError("q must hold the batch's rows")
+    buf = (ctypes.c_void_p * len(ptrs))(*ptrs)
+    sc = (ctypes.c_float * (2 * G))(*k_scale, *v_scale)
+    at, step, sa = ctypes.addressof(buf), 8 * G, ctypes.addressof(sc)
+    st = lib.lsa_attend_fp4(at, at + 2 * step, at + 3 * step, at + 4 * step, at + 5 * step, sa, sa + 4 * G, H_q, H_kv, d,
+                            index_sets.data_ptr(), index_sets.shape[1], cb, G, at + step, _ptr(workspace),
+                            0 if workspace is None else workspace.nbytes, _ptr(dev_status), _stream(stream))
+    if st:
+        _check("lsa_attend_fp4", st)
 
 
 def lsa_merge_pairs(pairs: torch.Tensor, counts: torch.Tensor, k: int, out: torch.Tensor,

@@ -3,6 +3,7 @@
 // Every check that can be made on the host is made here, before any launch;
 // nothing in this file allocates device memory or synchronises.
 #include <cmath>
+#include <cstdint>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -827,6 +828,166 @@ lsa_status_t lsa_attend_fp8(const uint16_t* const* q, const uint8_t* const* k_ca
     return attend_impl(q, reinterpret_cast<const void* const*>(k_cache), reinterpret_cast<const void* const*>(v_cache),
                        k_scale, v_scale, H_q, H_kv, d, index_sets, budget, batch, layers_per_index, out, nullptr,
                        workspace, workspace_bytes, dev_status, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 4-bit caches
+static bool prompts_ok(const lsa_prompts_t* p) {
+    if (p == nullptr) return false;
+    if (p->n_seq < 1 || p->n_rows < 0 || p->max_len < 1 || p->reserved != 0 || p->total_tokens < 0) return false;
+    return p->row_offset != nullptr && p->kv_offset != nullptr && p->seq_lens != nullptr &&
+           aligned(p->row_offset, 4) && aligned(p->kv_offset, 8) && aligned(p->seq_lens, 4);
+}
+
+// A power of two in [2^-100, 2^100].
+static bool layer_scale_ok(float s) {
+    int e = 0;
+    return std::isfinite(s) && s > 0.f && std::frexp(s, &e) == 0.5f && e >= -99 && e <= 101;
+}
+
+extern "C" {
+
+lsa_status_t lsa_store_fp4(const uint16_t* const* k_new, int64_t k_stride, const uint16_t* const* v_new,
+                           int64_t v_stride, int32_t H_kv, int32_t d, const lsa_prompts_t* prompts, int32_t layers,
+                           const float* k_scale, const float* v_scale, uint8_t* const* k, uint8_t* const* k_group,
+                           uint8_t* const* v, uint8_t* const* v_group, uint16_t* const* k_round,
+                           uint16_t* const* v_round, int32_t* dev_status, void* stream) {
+    if (!prompts_ok(prompts) || H_kv < 1 || d < 1 || layers < 1) return LSA_ERR_INVALID_ARG;
+    if (d != 128 || H_kv > 256 || layers > LSA_MAX_LAYERS) return LSA_ERR_UNSUPPORTED;
+    if (k_new == nullptr || v_new == nullptr || k == nullptr || k_group == nullptr || v == nullptr ||
+        v_group == nullptr || k_scale == nullptr || v_scale == nullptr || (k_round == nullptr) != (v_round == nullptr))
+        return LSA_ERR_INVALID_ARG;
+    if (k_stride < (int64_t)H_kv * d || v_stride < (int64_t)H_kv * d || k_stride % 8 != 0 || v_stride % 8 != 0)
+        return LSA_ERR_INVALID_ARG;
+    lsa::StoreFp4Args a;
+    std::memset(&a, 0, sizeof a);
+    for (int g = 0; g < layers; ++g) {
+        if (!layer_scale_ok(k_scale[g]) || !layer_scale_ok(v_scale[g])) return LSA_ERR_INVALID_ARG;
+        a.k_scale[g] = k_scale[g];
+        a.v_scale[g] = v_scale[g];
+    }
+    if (prompts->n_rows == 0) return LSA_OK;
+    if ((int64_t)prompts->n_rows * H_kv > (int64_t)INT32_MAX) return LSA_ERR_UNSUPPORTED;
+    for (int g = 0; g < layers; ++g) {
+        const void* need[] = {k_new[g], v_new[g], k[g], v[g]};
+        for (const void* p : need)
+            if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
+        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 8) || !aligned(v_group[g], 8))
+            return LSA_ERR_INVALID_ARG;
+        a.k_new[g] = k_new[g];
+        a.v_new[g] = v_new[g];
+        a.k[g] = k[g];
+        a.v[g] = v[g];
+        a.k_group[g] = k_group[g];
+        a.v_group[g] = v_group[g];
+        if (k_round != nullptr) {
+            if (k_round[g] == nullptr || v_round[g] == nullptr || !aligned(k_round[g], 16) || !aligned(v_round[g], 16))
+                return LSA_ERR_INVALID_ARG;
+            a.k_round[g] = k_round[g];
+            a.v_round[g] = v_round[g];
+        }
+    }
+    a.values = k_round != nullptr ? 1 : 0;
+    a.row_offset = prompts->row_offset;
+    a.kv_offset = prompts->kv_offset;
+    a.seq_lens = prompts->seq_lens;
+    a.dev_status = dev_status;
+    a.total_tokens = prompts->total_tokens;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_seq = prompts->n_seq;
+    a.n_rows = prompts->n_rows;
+    a.max_len = prompts->max_len;
+    a.H_kv = H_kv;
+    a.layers = layers;
+    cudaError_t e = lsa::launch_store_fp4(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LSA_OK : cuda_fail(e);
+}
+
+size_t lsa_attend_fp4_workspace_size(const lsa_batch_t* batch, int32_t H_q, int32_t H_kv, int32_t d, int32_t budget,
+                                     int32_t layers_per_index) {
+    if (batch == nullptr || batch->n_q <= 0 || batch->max_len < 1) return 0;
+    if (!attend_shape_ok(H_q, H_kv, d, budget, layers_per_index)) return 0;
+    return lsa::plan_attend_fp4(batch->n_q, H_q, H_kv, budget, layers_per_index, lsa::device_sm_count()).ws_bytes;
+}
+
+int32_t lsa_attend_fp4_launches(const lsa_batch_t* batch, int32_t H_q, int32_t H_kv, int32_t d, int32_t budget,
+                                int32_t layers_per_index) {
+    if (batch == nullptr || batch->n_q <= 0 || !attend_shape_ok(H_q, H_kv, d, budget, layers_per_index)) return 0;
+    const lsa::AttendPlan p =
+        lsa::plan_attend_fp4(batch->n_q, H_q, H_kv, budget, layers_per_index, lsa::device_sm_count());
+    return p.n_splits > 1 ? 2 : 1;
+}
+
+lsa_status_t lsa_attend_fp4(const uint16_t* const* q, const uint8_t* const* k, const uint8_t* const* k_group,
+                            const uint8_t* const* v, const uint8_t* const* v_group, const float* k_scale,
+                            const float* v_scale, int32_t H_q, int32_t H_kv, int32_t d, const int32_t* index_sets,
+                            int32_t budget, const lsa_batch_t* batch, int32_t layers_per_index, float* const* out,
+                            void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    if (!batch_ok(batch, true)) return LSA_ERR_INVALID_ARG;
+    if (H_q < 1 || H_kv < 1 || d < 1 || budget < 0 || layers_per_index < 1 || H_q % H_kv != 0)
+        return LSA_ERR_INVALID_ARG;
+    if (!attend_shape_ok(H_q, H_kv, d, budget, layers_per_index)) return LSA_ERR_UNSUPPORTED;
+    if (q == nullptr || k == nullptr || k_group == nullptr || v == nullptr || v_group == nullptr ||
+        k_scale == nullptr || v_scale == nullptr || out == nullptr)
+        return LSA_ERR_INVALID_ARG;
+    lsa::AttendFp4Args a;
+    std::memset(&a, 0, sizeof a);
+    lsa::AttendArgs& b = a.base;
+    for (int g = 0; g < layers_per_index; ++g) {
+        if (!std::isfinite(k_scale[g]) || !std::isfinite(v_scale[g])) return LSA_ERR_INVALID_ARG;
+        b.kscale[g] = k_scale[g];
+        b.vscale[g] = v_scale[g];
+    }
+    if (batch->n_q == 0) return LSA_OK;
+    if (budget > 0 && (index_sets == nullptr || !aligned(index_sets, 4))) return LSA_ERR_INVALID_ARG;
+    for (int g = 0; g < layers_per_index; ++g) {
+        const void* need[] = {q[g], k[g], v[g], out[g]};
+        for (const void* p : need)
+            if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
+        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 8) || !aligned(v_group[g], 8))
+            return LSA_ERR_INVALID_ARG;
+        b.q[g] = q[g];
+        b.out[g] = out[g];
+        a.k[g] = k[g];
+        a.k_group[g] = k_group[g];
+        a.v[g] = v[g];
+        a.v_group[g] = v_group[g];
+    }
+    if (batch->n_q > 65535) return LSA_ERR_UNSUPPORTED;
+    const lsa::AttendPlan p =
+        lsa::plan_attend_fp4(batch->n_q, H_q, H_kv, budget, layers_per_index, lsa::device_sm_count());
+    if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
+        return LSA_ERR_WORKSPACE;
+    b.sets = index_sets;
+    b.kv_offset = batch->kv_offset;
+    b.seq_lens = batch->seq_lens;
+    b.q_seq = batch->q_seq;
+    b.q_len = batch->q_len;
+    b.dev_status = dev_status;
+    if (p.n_splits > 1) {
+        const size_t rows_q = (size_t)layers_per_index * batch->n_q;
+        b.part_o = static_cast<float*>(workspace);
+        b.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                             (rows_q * p.n_splits * H_q * 128 * 4 + 255) / 256 * 256);
+    }
+    b.total_tokens = batch->total_tokens;
+    b.n_seq = batch->n_seq;
+    b.n_q = batch->n_q;
+    b.max_len = batch->max_len;
+    b.H_q = H_q;
+    b.H_kv = H_kv;
+    b.budget = budget;
+    b.G = layers_per_index;
+    b.n_splits = p.n_splits;
+    b.entries_per_split = p.entries_per_split;
+    b.head_groups = p.head_groups;
+    b.hpc = p.hpc;
+    b.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+    cudaError_t e = lsa::launch_attend_fp4(a, p.smem_bytes, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LSA_OK : cuda_fail(e);
 }
 
 }  // extern "C"

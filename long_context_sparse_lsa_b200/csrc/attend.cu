@@ -1077,6 +1077,13 @@ AttendPlan plan_attend_grouped(int n_q, int group_rows, int H_q, int H_kv, int b
     return p;
 }
 
+cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t stream) {
+    int nw = (a.n_splits + kMergeSplitsPerWarp - 1) / kMergeSplitsPerWarp;
+    if (nw > kMergeMaxWarps) nw = kMergeMaxWarps;
+    return launch_pdl(attend_merge_kernel, dim3((unsigned)a.H_q, (unsigned)a.n_q, (unsigned)a.G),
+                      dim3((unsigned)(nw * kWarp)), 0, stream, 0, a);
+}
+
 cudaError_t launch_attend_grouped(const AttendArgs& a, size_t smem_bytes, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(attend_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem_bytes);
@@ -1088,10 +1095,7 @@ cudaError_t launch_attend_grouped(const AttendArgs& a, size_t smem_bytes, cudaSt
                     (unsigned)(a.n_q / a.group_rows), (unsigned)a.G);
     e = launch_pdl(attend_group_kernel, grid, dim3(kConsumers * kWarp), smem_bytes, stream, 0, a);
     if (e != cudaSuccess || a.n_splits == 1) return e;
-    int nw = (a.n_splits + kMergeSplitsPerWarp - 1) / kMergeSplitsPerWarp;
-    if (nw > kMergeMaxWarps) nw = kMergeMaxWarps;
-    return launch_pdl(attend_merge_kernel, dim3((unsigned)a.H_q, (unsigned)a.n_q, (unsigned)a.G),
-                      dim3((unsigned)(nw * kWarp)), 0, stream, 0, a);
+    return launch_attend_merge(a, stream);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, size_t smem_bytes, cudaStream_t stream) {
@@ -1119,10 +1123,7 @@ cudaError_t launch_attend(const AttendArgs& a, size_t smem_bytes, cudaStream_t s
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.n_splits == 1) return e;
-    int nw = (a.n_splits + kMergeSplitsPerWarp - 1) / kMergeSplitsPerWarp;
-    if (nw > kMergeMaxWarps) nw = kMergeMaxWarps;
-    return launch_pdl(attend_merge_kernel, dim3((unsigned)a.H_q, (unsigned)a.n_q, (unsigned)a.G),
-                      dim3((unsigned)(nw * kWarp)), 0, stream, 0, a);
+    return launch_attend_merge(a, stream);
 }
 
 }  // namespace lsa

@@ -227,6 +227,40 @@ cudaError_t launch_attend_grouped(const AttendArgs& a, size_t smem_bytes, cudaSt
 // lsa_attend_si's sink and window part (attend_window.cu), after the gather.
 cudaError_t launch_attend_window(const AttendArgs& a, cudaStream_t stream);
 
+// Combines the split partials of any of the attention kernels (part_o, part_ml).
+cudaError_t launch_attend_merge(const AttendArgs& a, cudaStream_t stream);
+
+// ---- 4-bit K/V caches (fp4.cuh) -----------------------------------------------
+struct AttendFp4Args {
+    AttendArgs base;  // k, v unused
+    const uint8_t* k[kMaxLayers];        // [total_tokens][H_kv][64] codes
+    const uint8_t* k_group[kMaxLayers];  // [total_tokens][H_kv][8] group scales
+    const uint8_t* v[kMaxLayers];
+    const uint8_t* v_group[kMaxLayers];
+};
+AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int num_sms);
+cudaError_t launch_attend_fp4(const AttendFp4Args& a, size_t smem_bytes, cudaStream_t stream);
+
+struct StoreFp4Args {
+    const uint16_t* k_new[kMaxLayers];  // [n_rows] rows of H_kv * 128 bf16, k_stride / v_stride elements apart
+    const uint16_t* v_new[kMaxLayers];
+    uint8_t* k[kMaxLayers];
+    uint8_t* k_group[kMaxLayers];
+    uint8_t* v[kMaxLayers];
+    uint8_t* v_group[kMaxLayers];
+    uint16_t* k_round[kMaxLayers];  // [n_rows][H_kv][128] or NULL
+    uint16_t* v_round[kMaxLayers];
+    float k_scale[kMaxLayers], v_scale[kMaxLayers];
+    const int32_t* row_offset;
+    const int64_t* kv_offset;
+    const int32_t* seq_lens;
+    int32_t* dev_status;
+    int64_t total_tokens;
+    int64_t k_stride, v_stride;
+    int32_t n_seq, n_rows, max_len, H_kv, layers, values;
+};
+cudaError_t launch_store_fp4(const StoreFp4Args& a, cudaStream_t stream);
+
 int device_sm_count();
 
 // Launches `kernel` with programmatic stream serialisation (the kernel calls
