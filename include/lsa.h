@@ -518,6 +518,42 @@ lsa_status_t lsa_attend_si(const uint16_t *const *q, const uint16_t *const *k_ca
                            int32_t *dev_status, void *stream);
 
 /* ----------------------------------------------------------------------- */
+/* Whole prompts: causal attention over every token                          */
+/* ----------------------------------------------------------------------- */
+/* The dense pass beside the sparse one: while a context fits the budget its
+ * index set is all of it, and a model's prompts are attended this way before
+ * (or instead of) sparse attention over the cache. For every row r of every
+ * sequence (lsa_prompts_t: whole prompts, their newest chunk, or one token)
+ * and query head h,
+ *    out[r][h] = softmax_j(q . k_j / sqrt(d)) v_j
+ * over the tokens j that the row sees; scale and GQA mapping as fixed at the
+ * top of this file. Sums and softmax statistics are fp32; the weights are
+ * rounded to bf16 for the product with V, and the output to bf16 (it feeds
+ * the output projection). A token that a row does not see never counts,
+ * whatever its K and V hold; one that it sees and that is not finite does.
+ *
+ * q        device bf16 [n_rows] rows of H_q * d elements, q_stride elements
+ *          from one row to the next.
+ * k, v     device bf16 [total_tokens] rows of H_kv * d elements, k_stride and
+ *          v_stride apart: the caches, or the prompts' own rows (then
+ *          kv_offset = row_offset). Strides are multiples of 8, at least the
+ *          row (more for views of one fused projection).
+ * out      device bf16 [n_rows][H_q][d].
+ * lse      device fp32 [n_rows][H_q] or NULL: ln sum_j exp(q . k_j / sqrt(d)).
+ * workspace lsa_attend_prompt_workspace_size() bytes (partials of few rows over
+ *          long caches; no initialisation needed; may be NULL when that is 0).
+ * All device pointers 16-byte aligned (lse 4). Supported: d == 128; H_q / H_kv
+ * a whole number up to 64; H_q <= 4096; n_rows * H_q < 2^31. One launch, plus
+ * a merge when the keys are split.
+ */
+size_t lsa_attend_prompt_workspace_size(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
+int32_t lsa_attend_prompt_launches(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
+lsa_status_t lsa_attend_prompt(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                               const uint16_t *v, int64_t v_stride, int32_t H_q, int32_t H_kv, int32_t d,
+                               const lsa_prompts_t *prompts, uint16_t *out, float *lse, void *workspace,
+                               size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ----------------------------------------------------------------------- */
 /* Draft rows sharing one gather                                             */
 /* ----------------------------------------------------------------------- */
 /* A decode step that verifies several draft tokens of a sequence at once

@@ -33,7 +33,8 @@ EXPORTS = ["lsa_version", "lsa_last_cuda_error", "lsa_status_string", "lsa_hi_bl
            "lsa_combine", "lsa_attend_grouped_workspace_size", "lsa_attend_grouped_launches", "lsa_attend_grouped",
            "lsa_attend_si_workspace_size", "lsa_attend_si_launches", "lsa_attend_si",
            "lsa_attend_noalloc", "lsa_append_index", "lsa_append_index_launches", "lsa_store_fp4",
-           "lsa_attend_fp4_workspace_size", "lsa_attend_fp4_launches", "lsa_attend_fp4"]
+           "lsa_attend_fp4_workspace_size", "lsa_attend_fp4_launches", "lsa_attend_fp4",
+           "lsa_attend_prompt_workspace_size", "lsa_attend_prompt_launches", "lsa_attend_prompt"]
 
 MERGE_ID_BITS = 24  # LSA_MERGE_ID_BITS
 
@@ -192,6 +193,13 @@ def load_library():
     lib.lsa_attend_fp4.restype = i32
     lib.lsa_attend_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, ctypes.POINTER(_Batch), i32, vp, vp,
                                    sz, vp, vp]
+    lib.lsa_attend_prompt_workspace_size.restype = sz
+    lib.lsa_attend_prompt_workspace_size.argtypes = [ctypes.POINTER(_Prompts), i32, i32, i32]
+    lib.lsa_attend_prompt_launches.restype = i32
+    lib.lsa_attend_prompt_launches.argtypes = [ctypes.POINTER(_Prompts), i32, i32, i32]
+    lib.lsa_attend_prompt.restype = i32
+    lib.lsa_attend_prompt.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, ctypes.POINTER(_Prompts), vp, vp, vp, sz, vp,
+                                      vp]
     lib.lsa_score_tokens.restype = i32
     lib.lsa_score_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp]
     lib.lsa_score_blocks.restype = i32
@@ -618,6 +626,42 @@ def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_sc
                             0 if workspace is None else workspace.nbytes, _ptr(dev_status), _stream(stream))
     if st:
         _check("lsa_attend_fp4", st)
+
+
+def lsa_attend_prompt_workspace_size(prompts: Prompts, H_q: int, H_kv: int, d: int) -> int:
+    return load_library().lsa_attend_prompt_workspace_size(prompts.c(), H_q, H_kv, d)
+
+
+def lsa_attend_prompt_launches(prompts: Prompts, H_q: int, H_kv: int, d: int) -> int:
+    """Kernel launches lsa_attend_prompt issues for this shape."""
+    return load_library().lsa_attend_prompt_launches(prompts.c(), H_q, H_kv, d)
+
+
+def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts: Prompts, out: torch.Tensor,
+                      workspace: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of the prompts' rows over every token each sees: q bf16 [n_rows, H_q, 128], k and v bf16
+    [T, H_kv, 128] (views whose rows are apart, as of a fused projection, are taken as they are), out bf16 [n_rows,
+    H_q, 128], lse fp32 [n_rows, H_q] or None."""
+    lib = load_library()
+    n_rows, H_q, d = q.shape
+    T, H_kv = k.shape[:2]
+    bf16 = torch.bfloat16
+    _here(q)
+    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or out.dtype is not bf16:
+        raise TypeError("q, k, v and out must be bfloat16 tensors")
+    if k.shape != (T, H_kv, d) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("k and v must be [T, H_kv, d], out contiguous [n_rows, H_q, d]")
+    if n_rows != prompts.n_rows or T < prompts.total_tokens:
+        raise ValueError("q must hold prompts.n_rows rows, k and v prompts.total_tokens")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n_rows, H_q) or not lse.is_contiguous()):
+        raise TypeError("lse must be a contiguous float32 [n_rows, H_q] tensor")
+    st = lib.lsa_attend_prompt(q.data_ptr(), _row_stride("q", q, H_q, d), k.data_ptr(), _row_stride("k", k, H_kv, d),
+                               v.data_ptr(), _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.c(), out.data_ptr(),
+                               _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                               _ptr(dev_status), _stream(stream))
+    if st:
+        _check("lsa_attend_prompt", st)
 
 
 def lsa_merge_pairs(pairs: torch.Tensor, counts: torch.Tensor, k: int, out: torch.Tensor,

@@ -990,4 +990,86 @@ lsa_status_t lsa_attend_fp4(const uint16_t* const* q, const uint8_t* const* k, c
     return e == cudaSuccess ? LSA_OK : cuda_fail(e);
 }
 
+// ---------------------------------------------------------------------------
+static bool prompt_shape_ok(int32_t H_q, int32_t H_kv, int32_t d) {
+    return d == 128 && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 64 && H_q <= 4096;
+}
+
+// Row tiles and splits as CTAs of one grid.
+static bool prompt_grid_ok(const lsa::PromptPlan& p, int32_t n_rows, int32_t H_q, int32_t H_kv) {
+    return (int64_t)p.slots * H_kv * p.n_splits <= INT32_MAX && (int64_t)n_rows * H_q <= INT32_MAX;
+}
+
+static lsa::PromptPlan prompt_plan(const lsa_prompts_t* p, int32_t H_q, int32_t H_kv) {
+    return lsa::plan_prompt(p->n_seq, p->n_rows, p->max_len, H_q, H_kv, lsa::device_sm_count());
+}
+
+size_t lsa_attend_prompt_workspace_size(const lsa_prompts_t* prompts, int32_t H_q, int32_t H_kv, int32_t d) {
+    if (prompts == nullptr || prompts->n_seq < 1 || prompts->n_rows < 1 || prompts->max_len < 1 ||
+        !prompt_shape_ok(H_q, H_kv, d))
+        return 0;
+    return prompt_plan(prompts, H_q, H_kv).ws_bytes;
+}
+
+int32_t lsa_attend_prompt_launches(const lsa_prompts_t* prompts, int32_t H_q, int32_t H_kv, int32_t d) {
+    if (prompts == nullptr || prompts->n_seq < 1 || prompts->n_rows < 1 || prompts->max_len < 1 ||
+        !prompt_shape_ok(H_q, H_kv, d))
+        return 0;
+    return prompt_plan(prompts, H_q, H_kv).n_splits > 1 ? 2 : 1;
+}
+
+lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, int32_t H_q, int32_t H_kv, int32_t d,
+                               const lsa_prompts_t* prompts, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    if (!prompts_ok(prompts) || H_q < 1 || H_kv < 1 || d < 1 || H_q % H_kv != 0) return LSA_ERR_INVALID_ARG;
+    if (!prompt_shape_ok(H_q, H_kv, d)) return LSA_ERR_UNSUPPORTED;
+    if (q_stride < (int64_t)H_q * d || k_stride < (int64_t)H_kv * d || v_stride < (int64_t)H_kv * d)
+        return LSA_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0) return LSA_ERR_INVALID_ARG;
+    if (prompts->n_rows == 0) return LSA_OK;
+    if (prompts->total_tokens < 1) return LSA_ERR_INVALID_ARG;
+    const void* need[] = {q, k, v, out};
+    for (const void* p : need)
+        if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
+    if (lse != nullptr && !aligned(lse, 4)) return LSA_ERR_INVALID_ARG;
+    const lsa::PromptPlan p = prompt_plan(prompts, H_q, H_kv);
+    // tensor-map coordinates are 32-bit, strides below 2^40 bytes
+    if (!prompt_grid_ok(p, prompts->n_rows, H_q, H_kv) || prompts->total_tokens > (int64_t)INT32_MAX - 256 ||
+        prompts->n_rows > INT32_MAX - 256 || q_stride >= (1ll << 38) || k_stride >= (1ll << 38) || v_stride >= (1ll << 38))
+        return LSA_ERR_UNSUPPORTED;
+    if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
+        return LSA_ERR_WORKSPACE;
+    lsa::PromptArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.lse = lse;
+    if (p.n_splits > 1) {
+        a.part_o = static_cast<float*>(workspace);
+        a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.off_ml);
+    }
+    a.row_offset = prompts->row_offset;
+    a.kv_offset = prompts->kv_offset;
+    a.seq_lens = prompts->seq_lens;
+    a.dev_status = dev_status;
+    a.total_tokens = prompts->total_tokens;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_seq = prompts->n_seq;
+    a.n_rows = prompts->n_rows;
+    a.max_len = prompts->max_len;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.G = p.G;
+    a.tile_tokens = p.tile_tokens;
+    a.n_splits = p.n_splits;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+    cudaError_t e = lsa::launch_attend_prompt(a, p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LSA_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -174,6 +174,23 @@ __device__ __forceinline__ uint32_t warp_append(uint32_t* count, bool take) {
     return take ? base + (uint32_t)__popc(m & lanemask_lt()) : 0xffffffffu;
 }
 
+// The last i in [0, n) with le(i), for an le that holds up to some i and not
+// beyond (0 when it holds nowhere): 32 candidates a step. The whole warp calls
+// it with the same arguments.
+template <typename Le>
+__device__ __forceinline__ int find_last(int n, Le le) {
+    int lo = 0;  // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + (int)(threadIdx.x & 31) * step;
+        const int k = __popc(__ballot_sync(0xffffffffu, at < lo + n && le(at)));
+        const int skip = max(k - 1, 0) * step;
+        lo += skip;
+        n = min(step, n - skip);
+    }
+    return lo;
+}
+
 // 16-byte read-only global load.
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ uint2 ldg8(const void* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }

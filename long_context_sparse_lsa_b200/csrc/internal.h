@@ -261,6 +261,37 @@ struct StoreFp4Args {
 };
 cudaError_t launch_store_fp4(const StoreFp4Args& a, cudaStream_t stream);
 
+// ---- whole-prompt attention (attend_prompt.cu) ----------------------------------
+struct PromptArgs {
+    const uint16_t* q;  // [n_rows][H_q][128] bf16, rows q_stride elements apart
+    const uint16_t* k;  // [total_tokens][H_kv][128]
+    const uint16_t* v;
+    uint16_t* out;      // [n_rows][H_q][128]
+    float* lse;         // [n_rows][H_q] or NULL
+    float* part_o;      // [n_splits][n_rows][H_q][128]
+    float* part_ml;     // [n_splits][n_rows][H_q][2]
+    const int32_t* row_offset;
+    const int64_t* kv_offset;
+    const int32_t* seq_lens;
+    int32_t* dev_status;
+    int64_t total_tokens;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t n_seq, n_rows, max_len, H_q, H_kv;
+    int32_t G, tile_tokens, n_splits;  // query heads per kv head, tokens per row tile, key splits
+    float scale_log2;
+};
+struct PromptPlan {
+    int G = 1, tile_tokens = 128, slots = 0, n_splits = 1;
+    size_t off_ml = 0, ws_bytes = 0;
+};
+PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, int num_sms);
+cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream);
+// bf16 rows of H_kv * group heads of 128 channels, `stride` elements apart, in
+// boxes of 64 channels (128-byte swizzle): group == 0: one head of `tokens`
+// rows (3-D: channel, head, row); else the `group` query heads of one kv head
+// (4-D: channel, head of the group, kv head, row).
+bool tensor_map_rows_bf16(CUtensorMap* m, const void* base, int64_t rows, int H_kv, int group, int64_t stride, int tokens);
+
 int device_sm_count();
 
 // Launches `kernel` with programmatic stream serialisation (the kernel calls

@@ -91,22 +91,6 @@ __device__ __forceinline__ void quantise(const Groups16& in, float S, float inv_
     }
 }
 
-// Sequence whose rows hold `row`: the last b with row_offset[b] <= row (32
-// candidates a step, the whole warp calls it with the same row).
-__device__ __forceinline__ int find_seq(const int32_t* row_offset, int n_seq, int row) {
-    int lo = 0, n = n_seq;  // the answer lies in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int at = lo + lane_id() * step;
-        const bool le = at < lo + n && row_offset[at] <= row;
-        const int k = __popc(__ballot_sync(0xffffffffu, le));
-        const int next = lo + max(k - 1, 0) * step;
-        n = min(step, lo + n - next);
-        lo = next;
-    }
-    return lo;
-}
-
 // grid: (runs of kStThreads groups, layers * 2): K of layer g at y = 2 g, V at 2 g + 1
 template <bool VALUES>
 __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_constant__ StoreFp4Args a) {
@@ -131,7 +115,7 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
     // cache rows of the CTA's tokens
     if (tid < kWarp) {
         const int last = min(a.n_rows - 1, (int)((g0 + kStThreads - 1) / per_row));
-        int seq = find_seq(a.row_offset, a.n_seq, row0);
+        int seq = find_last(a.n_seq, [&](int b) { return a.row_offset[b] <= row0; });
         for (int i = tid; i <= last - row0; i += kWarp) {
             const int r = row0 + i;
             while (seq + 1 < a.n_seq && a.row_offset[seq + 1] <= r) ++seq;

@@ -1,5 +1,6 @@
-// tensor_map.cu — 2-D TMA tensor maps over row-major [rows, 128] byte
-// matrices with the 128-byte swizzle (key caches, indexer queries).
+// tensor_map.cu — TMA tensor maps with the 128-byte swizzle: over row-major
+// [rows, 128] byte matrices (key caches, indexer queries) and over rows of
+// bf16 heads (Q, K and V of the whole-prompt attention).
 //
 // The encode function is the driver's, resolved at run time through the
 // runtime's entry-point query, so the library does not link libcuda.
@@ -45,6 +46,27 @@ bool make_map_impl(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box
 }  // namespace
 
 bool tensor_maps_available() { return encode_fn() != nullptr; }
+
+bool tensor_map_rows_bf16(CUtensorMap* m, const void* base, int64_t rows, int H_kv, int group, int64_t stride, int tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t row = (cuuint64_t)stride * 2, head = 256;
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (group == 0) {
+        const cuuint64_t dims[3] = {128, (cuuint64_t)H_kv, (cuuint64_t)rows};
+        const cuuint64_t strides[2] = {head, row};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)tokens};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    const cuuint64_t dims[4] = {128, (cuuint64_t)group, (cuuint64_t)H_kv, (cuuint64_t)rows};
+    const cuuint64_t strides[3] = {head, head * (cuuint64_t)group, row};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tokens};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool tensor_map_rows128(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
     return make_map_impl(m, base, rows, box_rows);

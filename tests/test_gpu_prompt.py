@@ -1,0 +1,237 @@
+"""lsa_attend_prompt on the GPU against softmax(q k^T / sqrt(d)) v in 64 bits.
+
+Tolerance, relative to the largest |V| that a row sees: a weight is rounded to bf16 (half a step, 2^-9 .. 2^-8 of itself), so
+that a mean of V rows moves by at most 2^-8 of the largest; the output's own rounding is 2^-8 of it at most (bf16 eps / 2);
+fp32 sums and ex2 are far below: 2^-7 together. Errors of single weights are independent, so the relative 2-norm stays below
+2^-8 / sqrt(3) for one weight and the output's 2^-8 / sqrt(3): 2^-8 together (sqrt(2 / 3) of 2^-8).
+The log-sum-exp is fp32: its sum's relative error (ex2: 2^-22, 128-key partial sums, the scores' 2^-24 * 128 * ~4) is below
+2^-15 and so its absolute error, plus 2^-23 of itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_sparse_lsa_b200 import binding as lsa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+MAX, L2, LSE = 2.0 ** -7, 2.0 ** -8, 2.0 ** -15
+
+
+def _rand(shape, seed, scale=1.0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device=DEV) * scale).to(torch.bfloat16)
+
+
+class Case:
+    def __init__(self, H, K, rows, lens, seed=0, gap=0, fused=False, scale=1.0, max_len=None):
+        ro, ko = [0], [gap]
+        for n, length in zip(rows, lens):
+            ro.append(ro[-1] + n)
+            ko.append(ko[-1] + length + gap)
+        self.H, self.K, self.rows, self.lens, self.ko, self.ro = H, K, rows, lens, ko[:-1], ro
+        self.n, self.total = ro[-1], ko[-1]
+        if fused:  # rows of one projection: Q, K, V and something else side by side
+            x = _rand((self.n, H + 2 * K + 1, 128), seed)
+            self.q, self.k, self.v = x[:, :H], x[:, H:H + K], x[:, H + K:H + 2 * K]
+        else:
+            self.q, self.k, self.v = (_rand((m, h, 128), seed + i) for i, (m, h) in
+                                      enumerate(((self.n, H), (self.total, K), (self.total, K))))
+        if scale != 1.0:
+            self.q.mul_(scale)
+        i32, i64 = (lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)), (lambda x: torch.tensor(x, dtype=torch.int64, device=DEV))
+        self.pr = lsa.Prompts(i32(ro), i64(ko[:-1]), i32(lens), self.n, max_len or max(max(lens), 1), self.total)
+        self.out = torch.full((self.n, H, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+        self.lse = torch.full((self.n, H), 9.0, device=DEV)
+        self.status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        size = lsa.lsa_attend_prompt_workspace_size(self.pr, H, K, 128)
+        self.ws = torch.full((max(size, 256),), 0xFF, dtype=torch.uint8, device=DEV)
+
+    def run(self, stream=None, lse=True):
+        lsa.lsa_attend_prompt(self.q, self.k, self.v, self.pr, self.out, self.ws, self.lse if lse else None, self.status,
+                              stream)
+        return self
+
+    def want(self, b):
+        """Output and log-sum-exp of sequence b's rows in 64 bits, and the largest |V| each row sees."""
+        n, length, o = self.rows[b], self.lens[b], self.ko[b]
+        q = self.q[self.ro[b]:self.ro[b] + n].double()
+        k, v = (x[o:o + length].double() for x in (self.k, self.v))
+        R = self.H // self.K
+        z = torch.einsum("rhd,thd->hrt", q, k.repeat_interleave(R, 1)) / 128 ** 0.5
+        hidden = torch.arange(length, device=DEV) > torch.arange(length - n, length, device=DEV)[:, None]
+        z.masked_fill_(hidden, -torch.inf)
+        lse = torch.logsumexp(z, -1)
+        p = torch.exp(z - lse[..., None])
+        # (a weight of 0 times a hidden V that is not finite is not part of the sum)
+        out = torch.empty_like(q)
+        clean = torch.nan_to_num(v, 0.0, 0.0, 0.0)
+        out = torch.einsum("hrt,thd->rhd", p, clean.repeat_interleave(R, 1))
+        for t, h, d in (~torch.isfinite(v)).nonzero().tolist():
+            first = max(0, t - (length - n))
+            out[first:, h * R:(h + 1) * R, d] += v[t, h, d]
+        return out, lse.T, float(clean.abs().max())
+
+    def check(self, skip=()):
+        assert self.status.item() == 0
+        for b, n in enumerate(self.rows):
+            if n == 0 or b in skip:
+                continue
+            want, lse, top = self.want(b)
+            got = self.out[self.ro[b]:self.ro[b] + n].double()
+            assert torch.equal(got.isnan(), want.isnan()), b
+            inf = want.isinf()
+            assert torch.equal(got[inf], want[inf]) and torch.equal(got.isinf(), inf), b
+            fine = want.isfinite()
+            diff = torch.where(fine, got - want, 0.0)
+            assert diff.abs().max() <= MAX * top, (b, float(diff.abs().max() / top))
+            ref = torch.where(fine, want, 0.0).norm()
+            assert diff.norm() <= L2 * ref, (b, float(diff.norm() / ref))
+            got_lse = self.lse[self.ro[b]:self.ro[b] + n].double()
+            assert torch.equal(got_lse.isnan(), lse.isnan())
+            assert (got_lse - lse).nan_to_num().abs().max() <= LSE + 2.0 ** -23 * lse.nan_to_num().abs().max(), b
+
+
+@pytest.mark.parametrize("H,K", [(1, 1), (8, 1), (16, 1), (4, 2), (32, 4), (4, 4), (6, 2), (5, 1), (28, 4), (64, 1), (12, 1)])
+def test_heads(H, K):
+    """Groups of 1 to 64 query heads, also ones that do not divide a tile."""
+    Case(H, K, [1, 2, 33, 129, 300], [1, 2, 33, 129, 300], seed=H + K).run().check()
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257, 511, 513, 1000])
+@pytest.mark.parametrize("H,K", [(8, 1), (2, 2)])
+def test_lengths(n, H, K):
+    Case(H, K, [n], [n], seed=n).run().check()
+
+
+@pytest.mark.parametrize("rows,lens", [
+    ([1] * 16, [3136 - 190 * i for i in range(16)]),           # one token each over ragged caches
+    ([1], [20000]), ([1], [1]), ([3], [5000]),                   # few rows, long caches: the keys are split
+    ([100, 0, 1, 64, 0], [700, 50, 1000, 64, 0]),                # sequences without rows, chunks, a whole prompt
+    ([513], [2000]), ([40] * 40, [40 + 13 * i for i in range(40)]),
+    ([1] * 1100, [1 + i % 7 for i in range(1100)]),              # more sequences than one search step holds
+])
+@pytest.mark.parametrize("gap", [0, 5])
+def test_caches(rows, lens, gap):
+    c = Case(8, 2, rows, lens, seed=len(rows), gap=gap)
+    c.run().check()
+    c.out.fill_(9.0)
+    c.run(lse=False).check()
+
+
+def test_long_prompt():
+    c = Case(8, 2, [5000], [5000], seed=3)
+    c.run().check()
+
+
+@pytest.mark.parametrize("rows,lens", [([70, 300, 1], [70, 300, 1]), ([2048], [2048])])
+def test_views_of_a_fused_projection(rows, lens):
+    Case(8, 2, rows, lens, fused=True, seed=9).run().check()
+
+
+@pytest.mark.parametrize("scale", [0.0, 30.0])
+def test_flat_and_peaked_softmax(scale):
+    """Equal scores, and scores that differ by hundreds (the running maximum moves often)."""
+    c = Case(8, 1, [700, 40], [700, 900], scale=scale or 1.0, seed=4)
+    if scale == 0.0:
+        c.q.zero_()
+    else:
+        c.k[:900] *= torch.linspace(0.1, 3, 900, device=DEV).to(torch.bfloat16)[:, None, None]  # later keys score higher
+    c.run()
+    if scale == 30.0:  # scores of size 1000 carry 2^-24 * 1000 * 8 in fp32: 2^-11 of a weight, still below its bf16 rounding
+        c.lse.copy_(torch.cat([c.want(b)[1] for b in range(2)]))
+    c.check()
+
+
+def test_rows_behind_and_other_sequences_hold_anything():
+    """Cache rows of no sequence hold NaN and infinities; rows of no sequence are left as they were."""
+    c = Case(8, 2, [100, 30, 257], [100, 95, 300], gap=200, seed=5)
+    used = torch.zeros(c.total, dtype=torch.bool, device=DEV)
+    for o, length in zip(c.ko, c.lens):
+        used[o:o + length] = True
+    c.k[~used] = float("nan")
+    c.v[~used] = float("inf")
+    c.run().check()
+    full = c.out.clone()
+    c.pr = lsa.Prompts(c.pr.row_offset[1:3].contiguous(), c.pr.kv_offset[1:2].contiguous(), c.pr.seq_lens[1:2].contiguous(),
+                       c.n, c.pr.max_len, c.total)
+    c.ws = torch.empty(max(256, lsa.lsa_attend_prompt_workspace_size(c.pr, 8, 2, 128)), dtype=torch.uint8, device=DEV)
+    c.out.fill_(9.0)
+    c.lse.fill_(9.0)
+    c.run()
+    assert (c.out[:100] == 9).all() and (c.out[130:] == 9).all() and (c.lse[:100] == 9).all() and (c.lse[130:] == 9).all()
+    assert (c.out[100:130].double() - full[100:130].double()).abs().max() <= 2 * MAX * 5
+
+
+@pytest.mark.parametrize("H,K,n,length", [(8, 1, 300, 300), (1, 1, 700, 800), (8, 1, 1, 4000), (64, 1, 9, 200)])
+def test_not_finite_where_it_is_seen(H, K, n, length):
+    """A K or V that is not finite reaches the rows that see it and no other."""
+    for where in (length - 1, max(0, length - n // 2 - 1), length - n):
+        c = Case(H, K, [n, 20], [length, 20], seed=6)
+        c.v[where, 0, 5], c.v[where, 0, 77], c.v[where, 0, 127] = float("inf"), float("nan"), float("-inf")
+        c.run().check()
+        c = Case(H, K, [n, 20], [length, 20], seed=7)
+        c.k[where, 0, 5] = float("nan")
+        c.run().check()
+    c = Case(H, K, [n, 20], [length, 20], seed=8)
+    c.q[n - 1, 0, 3] = float("nan")
+    c.run().check()
+
+
+@pytest.mark.parametrize("bad", ["rows", "cache", "negative", "max_len", "end"])
+@pytest.mark.parametrize("split", [False, True])
+def test_bad_sequences_are_skipped(bad, split):
+    long = 3000 if split else 60
+    c = Case(8, 1, [20, 30, 40] if not split else [1, 2, 1], [50, long, 45], seed=10)
+    pr, skip = c.pr, 1
+    if bad == "rows":
+        pr.seq_lens[1] = c.rows[1] - 1
+    elif bad == "cache":
+        pr.kv_offset[1] = c.total - long + 1
+    elif bad == "negative":
+        pr.kv_offset[1] = -1
+    elif bad == "max_len":
+        pr.seq_lens[1] = pr.max_len + 1
+        pr.total_tokens += 0
+    else:
+        pr.row_offset[3] += 1
+        skip = 2
+    c.run()
+    assert c.status.item() == lsa.LSA_DEV_BAD_LENGTH
+    lo, hi = c.ro[skip], c.ro[skip + 1]
+    assert (c.out[lo:hi] == 9).all() and (c.lse[lo:hi] == 9).all()
+    c.status.zero_()
+    c.check(skip=(skip,))
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    a, b = Case(8, 2, [600], [600], seed=1), Case(8, 2, [2], [6000], seed=2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a.run(s1)
+        b.run(s2)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        b.run()
+        a.run()
+    for seed in (5, 6):
+        a.q.copy_(_rand((600, 8, 128), seed))
+        b.v.copy_(_rand((6000, 2, 128), seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        a.check()
+        b.check()
+
+
+def test_same_bits_every_time():
+    for rows, lens in (([700, 300], [700, 900]), ([1, 1], [5000, 4000])):
+        c = Case(8, 2, rows, lens).run()
+        first, lse = c.out.clone(), c.lse.clone()
+        for _ in range(5):
+            c.run()
+            assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
