@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -67,6 +68,11 @@ class _Prompts(ctypes.Structure):
                 ("row_offset", ctypes.c_void_p), ("kv_offset", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
 
 
+# the same two structures for struct.pack (native alignment)
+_BATCH, _PROMPTS = struct.Struct("@4iq5P"), struct.Struct("@4iq3P")
+assert _BATCH.size == ctypes.sizeof(_Batch) and _PROMPTS.size == ctypes.sizeof(_Prompts)
+
+
 @dataclass
 class Budget:
     sink: int
@@ -94,17 +100,22 @@ class Batch:
     total_tokens: int
     blk_offset: torch.Tensor | None = None  # int64 [n_seq]
 
-    def c(self) -> _Batch:
-        for name, t, dt in (("kv_offset", self.kv_offset, torch.int64), ("seq_lens", self.seq_lens, torch.int32),
-                            ("q_seq", self.q_seq, torch.int32), ("q_len", self.q_len, torch.int32)):
-            if t.dtype != dt or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous {dt} tensor")
-        if self.blk_offset is not None and (self.blk_offset.dtype != torch.int64 or not self.blk_offset.is_contiguous()):
+    def packed(self) -> bytes:
+        """lsa_batch_t as bytes (cheaper to build and to pass than a ctypes structure)."""
+        ko, sl, qs, ql, bo = self.kv_offset, self.seq_lens, self.q_seq, self.q_len, self.blk_offset
+        i32, i64 = torch.int32, torch.int64
+        if not (ko.dtype is i64 and sl.dtype is i32 and qs.dtype is i32 and ql.dtype is i32 and ko.is_contiguous()
+                and sl.is_contiguous() and qs.is_contiguous() and ql.is_contiguous()):
+            for name, t, dt in (("kv_offset", ko, i64), ("seq_lens", sl, i32), ("q_seq", qs, i32), ("q_len", ql, i32)):
+                if t.dtype != dt or not t.is_contiguous():
+                    raise TypeError(f"{name} must be a contiguous {dt} tensor")
+        if bo is not None and (bo.dtype is not i64 or not bo.is_contiguous()):
             raise TypeError("blk_offset must be a contiguous int64 tensor")
-        return _Batch(int(self.seq_lens.numel()), int(self.q_seq.numel()), int(self.max_len), 0,
-                      int(self.total_tokens), self.kv_offset.data_ptr(), self.seq_lens.data_ptr(),
-                      self.blk_offset.data_ptr() if self.blk_offset is not None else None,
-                      self.q_seq.data_ptr(), self.q_len.data_ptr())
+        return _BATCH.pack(sl.numel(), qs.numel(), int(self.max_len), 0, int(self.total_tokens), ko.data_ptr(),
+                           sl.data_ptr(), 0 if bo is None else bo.data_ptr(), qs.data_ptr(), ql.data_ptr())
+
+    def c(self) -> _Batch:
+        return _Batch.from_buffer_copy(self.packed())
 
 
 @dataclass
@@ -119,7 +130,8 @@ class Prompts:
     max_len: int
     total_tokens: int
 
-    def c(self) -> _Prompts:
+    def packed(self) -> bytes:
+        """lsa_prompts_t as bytes."""
         ro, ko, sl = self.row_offset, self.kv_offset, self.seq_lens
         if (ro.dtype is not torch.int32 or ko.dtype is not torch.int64 or sl.dtype is not torch.int32
                 or not (ro.is_contiguous() and ko.is_contiguous() and sl.is_contiguous())):
@@ -127,8 +139,11 @@ class Prompts:
         n_seq = sl.numel()
         if ro.numel() != n_seq + 1 or ko.numel() != n_seq:
             raise ValueError("row_offset must hold n_seq + 1 values, kv_offset and seq_lens n_seq")
-        return _Prompts(n_seq, self.n_rows, self.max_len, 0, self.total_tokens, ro.data_ptr(), ko.data_ptr(),
-                        sl.data_ptr())
+        return _PROMPTS.pack(n_seq, self.n_rows, self.max_len, 0, self.total_tokens, ro.data_ptr(), ko.data_ptr(),
+                             sl.data_ptr())
+
+    def c(self) -> _Prompts:
+        return _Prompts.from_buffer_copy(self.packed())
 
 
 _lib = None
@@ -184,22 +199,20 @@ def load_library():
                                    ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), i32, i32, i32, vp,
                                    i32, ctypes.POINTER(_Batch), i32, ctypes.POINTER(vp), vp, sz, vp, vp]
     lib.lsa_store_fp4.restype = i32
-    lib.lsa_store_fp4.argtypes = [vp, i64, vp, i64, i32, i32, ctypes.POINTER(_Prompts), i32, vp, vp, vp, vp, vp, vp, vp,
+    lib.lsa_store_fp4.argtypes = [vp, i64, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                   vp, vp, vp]
     lib.lsa_attend_fp4_workspace_size.restype = sz
     lib.lsa_attend_fp4_workspace_size.argtypes = [ctypes.POINTER(_Batch), i32, i32, i32, i32, i32]
     lib.lsa_attend_fp4_launches.restype = i32
     lib.lsa_attend_fp4_launches.argtypes = [ctypes.POINTER(_Batch), i32, i32, i32, i32, i32]
     lib.lsa_attend_fp4.restype = i32
-    lib.lsa_attend_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, ctypes.POINTER(_Batch), i32, vp, vp,
-                                   sz, vp, vp]
+    lib.lsa_attend_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp, vp]
     lib.lsa_attend_prompt_workspace_size.restype = sz
     lib.lsa_attend_prompt_workspace_size.argtypes = [ctypes.POINTER(_Prompts), i32, i32, i32]
     lib.lsa_attend_prompt_launches.restype = i32
     lib.lsa_attend_prompt_launches.argtypes = [ctypes.POINTER(_Prompts), i32, i32, i32]
     lib.lsa_attend_prompt.restype = i32
-    lib.lsa_attend_prompt.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, ctypes.POINTER(_Prompts), vp, vp, vp, sz, vp,
-                                      vp]
+    lib.lsa_attend_prompt.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
     lib.lsa_score_tokens.restype = i32
     lib.lsa_score_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp]
     lib.lsa_score_blocks.restype = i32
@@ -240,8 +253,8 @@ def _check(func: str, status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the 3 us of the stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -519,18 +532,52 @@ def lsa_attend_noalloc(q: list, k: list, v: list, index_sets: torch.Tensor, batc
 
 def _here(t: torch.Tensor) -> None:
     """Refuse tensors that are not on the device the call would run on."""
-    if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device")
 
 
-def _layers(name: str, ts: list, n: int, dtype: torch.dtype, shape: tuple) -> list:
-    """The device pointers of a per-layer list of contiguous tensors."""
+_POINTERS = [struct.Struct(f"@{n}P") for n in range(9)]  # a host array of up to LSA_MAX_LAYERS device pointers
+_FLOATS = [struct.Struct(f"@{n}f") for n in range(9)]
+
+
+def _layers(name: str, ts: list, n: int, dtype: torch.dtype, shape: tuple) -> bytes:
+    """The device pointers of a per-layer list of contiguous tensors, as a host array."""
     if len(ts) != n:
         raise ValueError(f"{name} must hold one tensor per layer")
+    ptrs = []
     for t in ts:
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise TypeError(f"{name} must hold contiguous {dtype} tensors of shape {shape}")
-    return [t.data_ptr() for t in ts]
+        ptrs.append(t.data_ptr())
+    return _POINTERS[n].pack(*ptrs)
+
+
+def _layer_count(ts: list) -> int:
+    if not 1 <= len(ts) <= 8:
+        raise ValueError("1 to 8 layers")
+    return len(ts)
+
+
+def _scales(k_scale: list, v_scale: list, n: int) -> tuple[bytes, bytes]:
+    if len(k_scale) != n or len(v_scale) != n:
+        raise ValueError("k_scale and v_scale must hold one scale per layer")
+    return _FLOATS[n].pack(*k_scale), _FLOATS[n].pack(*v_scale)
+
+
+def _rows(name: str, ts: list, n: int, shape: tuple) -> tuple[bytes, int]:
+    """Device pointers and row stride of a per-layer list of bf16 [rows, H, d] views, all with the same stride."""
+    if len(ts) != n:
+        raise ValueError(f"{name} must hold one tensor per layer")
+    ptrs, stride = [], None
+    for t in ts:
+        if t.dtype is not torch.bfloat16 or t.shape != shape:
+            raise TypeError(f"{name} must hold bfloat16 tensors of shape {shape}")
+        s = _row_stride(name, t, shape[1], shape[2])
+        if stride is not None and s != stride:
+            raise ValueError(f"{name}: every layer must have the same row stride")
+        stride = s
+        ptrs.append(t.data_ptr())
+    return _POINTERS[n].pack(*ptrs), stride
 
 
 def _row_stride(name: str, t: torch.Tensor, H: int, d: int) -> int:
@@ -549,39 +596,26 @@ def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_g
     [T, H_kv, 8]) with per-layer power-of-two scales. k_round, v_round: the values the caches now hold (bf16
     [n_rows, H_kv, 128])."""
     lib = load_library()
-    G = len(k_new)
-    n_rows, H_kv, d = k_new[0].shape
+    G = _layer_count(k_new)
+    rows = tuple(k_new[0].shape)
+    n_rows, H_kv, d = rows
     T = k[0].shape[0]
     _here(k_new[0])
     if n_rows != prompts.n_rows or T < prompts.total_tokens:
         raise ValueError("k_new must hold prompts.n_rows rows and the caches prompts.total_tokens")
-    strides, ptrs = [], []
-    for name, ts in (("k_new", k_new), ("v_new", v_new)):
-        if len(ts) != G:
-            raise ValueError(f"{name} must hold one tensor per layer")
-        for t in ts:
-            if t.dtype is not torch.bfloat16 or t.shape != (n_rows, H_kv, d):
-                raise TypeError(f"{name} must hold bfloat16 [n_rows, H_kv, d] tensors")
-            strides.append(_row_stride(name, t, H_kv, d))
-            ptrs.append(t.data_ptr())
-        if len(set(strides[-G:])) > 1:
-            raise ValueError(f"{name}: every layer must have the same row stride")
-    u8 = torch.uint8
-    ptrs += _layers("k", k, G, u8, (T, H_kv, d // 2)) + _layers("k_group", k_group, G, u8, (T, H_kv, d // 16))
-    ptrs += _layers("v", v, G, u8, (T, H_kv, d // 2)) + _layers("v_group", v_group, G, u8, (T, H_kv, d // 16))
+    kn, k_stride = _rows("k_new", k_new, G, rows)
+    vn, v_stride = _rows("v_new", v_new, G, rows)
+    u8, code, group = torch.uint8, (T, H_kv, d // 2), (T, H_kv, d // 16)
     if (k_round is None) != (v_round is None):
         raise ValueError("k_round and v_round come together")
+    kr = vr = None
     if k_round is not None:
-        ptrs += _layers("k_round", k_round, G, torch.bfloat16, (n_rows, H_kv, d))
-        ptrs += _layers("v_round", v_round, G, torch.bfloat16, (n_rows, H_kv, d))
-    if len(k_scale) != G or len(v_scale) != G:
-        raise ValueError("k_scale and v_scale must hold one scale per layer")
-    buf = (ctypes.c_void_p * len(ptrs))(*ptrs)
-    sc = (ctypes.c_float * (2 * G))(*k_scale, *v_scale)
-    at, step, sa = ctypes.addressof(buf), 8 * G, ctypes.addressof(sc)
-    rounds = (None, None) if k_round is None else (at + 6 * step, at + 7 * step)
-    st = lib.lsa_store_fp4(at, strides[0], at + step, strides[G], H_kv, d, prompts.c(), G, sa, sa + 4 * G, at + 2 * step,
-                           at + 3 * step, at + 4 * step, at + 5 * step, *rounds, _ptr(dev_status), _stream(stream))
+        kr = _layers("k_round", k_round, G, torch.bfloat16, rows)
+        vr = _layers("v_round", v_round, G, torch.bfloat16, rows)
+    st = lib.lsa_store_fp4(kn, k_stride, vn, v_stride, H_kv, d, prompts.packed(), G, *_scales(k_scale, v_scale, G),
+                           _layers("k", k, G, u8, code), _layers("k_group", k_group, G, u8, group),
+                           _layers("v", v, G, u8, code), _layers("v_group", v_group, G, u8, group), kr, vr,
+                           None if dev_status is None else dev_status.data_ptr(), _stream(stream))
     if st:
         _check("lsa_store_fp4", st)
 
@@ -601,29 +635,24 @@ def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_sc
     """lsa_attend over 4-bit K/V caches: codes uint8 [T, H_kv, 64], group scales uint8 E4M3 [T, H_kv, 8], per-layer
     scales (lists of G tensors and floats)."""
     lib = load_library()
-    G = len(q)
-    n_q, H_q, d = q[0].shape
-    T, H_kv = k[0].shape[:2]
+    G = _layer_count(q)
+    rows = tuple(q[0].shape)
+    n_q, H_q, d = rows
+    T, H_kv, _ = k[0].shape
     _here(q[0])
     if index_sets.dtype is not torch.int32 or not index_sets.is_contiguous() or index_sets.shape[0] != n_q:
         raise TypeError("index_sets must be a contiguous int32 [n_q, budget] tensor")
-    if T < batch.total_tokens:
-        raise ValueError("the caches must hold batch.total_tokens rows")
-    if len(k_scale) != G or len(v_scale) != G:
-        raise ValueError("k_scale and v_scale must hold one scale per layer")
-    u8, rows = torch.uint8, (n_q, H_q, d)
-    ptrs = _layers("q", q, G, torch.bfloat16, rows) + _layers("out", out, G, torch.float32, rows)
-    ptrs += _layers("k", k, G, u8, (T, H_kv, d // 2)) + _layers("k_group", k_group, G, u8, (T, H_kv, d // 16))
-    ptrs += _layers("v", v, G, u8, (T, H_kv, d // 2)) + _layers("v_group", v_group, G, u8, (T, H_kv, d // 16))
-    cb = batch.c()
-    if cb.n_q != n_q:
-        raise ValueError("q must hold the batch's rows")
-    buf = (ctypes.c_void_p * len(ptrs))(*ptrs)
-    sc = (ctypes.c_float * (2 * G))(*k_scale, *v_scale)
-    at, step, sa = ctypes.addressof(buf), 8 * G, ctypes.addressof(sc)
-    st = lib.lsa_attend_fp4(at, at + 2 * step, at + 3 * step, at + 4 * step, at + 5 * step, sa, sa + 4 * G, H_q, H_kv, d,
-                            index_sets.data_ptr(), index_sets.shape[1], cb, G, at + step, _ptr(workspace),
-                            0 if workspace is None else workspace.nbytes, _ptr(dev_status), _stream(stream))
+    if T < batch.total_tokens or batch.q_seq.numel() != n_q:
+        raise ValueError("the caches must hold batch.total_tokens rows, q the batch's rows")
+    u8, code, group = torch.uint8, (T, H_kv, d // 2), (T, H_kv, d // 16)
+    st = lib.lsa_attend_fp4(_layers("q", q, G, torch.bfloat16, rows), _layers("k", k, G, u8, code),
+                            _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
+                            _layers("v_group", v_group, G, u8, group), *_scales(k_scale, v_scale, G), H_q, H_kv, d,
+                            index_sets.data_ptr(), index_sets.shape[1], batch.packed(), G,
+                            _layers("out", out, G, torch.float32, rows),
+                            None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.nbytes,
+                            None if dev_status is None else dev_status.data_ptr(), _stream(stream))
     if st:
         _check("lsa_attend_fp4", st)
 
@@ -657,7 +686,7 @@ def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n_rows, H_q) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 [n_rows, H_q] tensor")
     st = lib.lsa_attend_prompt(q.data_ptr(), _row_stride("q", q, H_q, d), k.data_ptr(), _row_stride("k", k, H_kv, d),
-                               v.data_ptr(), _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.c(), out.data_ptr(),
+                               v.data_ptr(), _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.packed(), out.data_ptr(),
                                _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
                                _ptr(dev_status), _stream(stream))
     if st:

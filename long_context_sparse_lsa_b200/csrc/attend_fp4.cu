@@ -411,8 +411,10 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
 
 cudaError_t launch_attend_fp4(const AttendFp4Args& a, size_t smem_bytes, cudaStream_t stream) {
     const AttendArgs& b = a.base;
-    auto kern = b.H_q / b.H_kv <= 8 ? attend_fp4_kernel<1> : attend_fp4_kernel<2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes);
+    static std::atomic<uint64_t> allowed[2];
+    const int wide = b.H_q / b.H_kv > 8;
+    auto kern = wide ? attend_fp4_kernel<2> : attend_fp4_kernel<1>;
+    cudaError_t e = allow_smem(kern, kF4RingBytes + 4 * kF4MaxEntries, allowed[wide]);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(b.n_splits * b.head_groups), (unsigned)b.n_q, (unsigned)b.G);
     e = launch_pdl(kern, grid, dim3(kF4Threads), smem_bytes, stream, 0, a);

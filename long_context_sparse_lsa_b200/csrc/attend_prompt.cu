@@ -507,7 +507,8 @@ cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaS
         !tensor_map_rows_bf16(&args.k, a.k, a.total_tokens, a.H_kv, 0, a.k_stride, kPrKeys) ||
         !tensor_map_rows_bf16(&args.v, a.v, a.total_tokens, a.H_kv, 0, a.v_stride, kPrKeys))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attend_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(attend_prompt_kernel, kPrSmem, allowed);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attend_prompt_kernel, dim3((unsigned)((int64_t)p.slots * a.H_kv * p.n_splits)), dim3(kPrThreads), kPrSmem,
                    stream, 0, args);

@@ -2,6 +2,7 @@
 // (abi.cu) and the kernel translation units. Host and device code only.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -293,6 +294,21 @@ cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaS
 bool tensor_map_rows_bf16(CUtensorMap* m, const void* base, int64_t rows, int H_kv, int group, int64_t stride, int tokens);
 
 int device_sm_count();
+
+// Lets `kernel` take up to `bytes` of dynamic shared memory. The attribute
+// stays with the kernel on its device, so it is set once per device (`done`:
+// one bit each, a static of the caller; setting it twice does no harm).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launches `kernel` with programmatic stream serialisation (the kernel calls
 // pdl_enter() first) and, when cluster > 0, that cluster size along x.

@@ -48,6 +48,10 @@ def _prompts(**kw):
     return lsa._Prompts(*[f[n] for n, _ in lsa._Prompts._fields_])
 
 
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
 def _ptrs(*xs):
     return ctypes.addressof(_ptrs.keep.setdefault(xs, (ctypes.c_void_p * len(xs))(*xs)))
 
@@ -67,7 +71,7 @@ def _store(**kw):
     a = dict(kn=two, ks=512, vn=two, vs=512, H=4, d=128, prompts=_prompts(), layers=2, ksc=_scales(1.0, 0.5),
              vsc=_scales(1.0, 2.0 ** -100), k=two, kg=two, v=two, vg=two, kr=None, vr=None)
     a.update(kw)
-    return lsa.load_library().lsa_store_fp4(a["kn"], a["ks"], a["vn"], a["vs"], a["H"], a["d"], a["prompts"], a["layers"],
+    return lsa.load_library().lsa_store_fp4(a["kn"], a["ks"], a["vn"], a["vs"], a["H"], a["d"], _ref(a["prompts"]), a["layers"],
                                             a["ksc"], a["vsc"], a["k"], a["kg"], a["v"], a["vg"], a["kr"], a["vr"], None,
                                             None)
 
@@ -103,7 +107,7 @@ def _attend(**kw):
              budget=3136, batch=b, G=2, out=two, ws=None, nb=0)
     a.update(kw)
     return lsa.load_library().lsa_attend_fp4(a["q"], a["k"], a["kg"], a["v"], a["vg"], a["ksc"], a["vsc"], a["H"], a["K"],
-                                             a["d"], a["sets"], a["budget"], a["batch"], a["G"], a["out"], a["ws"],
+                                             a["d"], a["sets"], a["budget"], _ref(a["batch"]), a["G"], a["out"], a["ws"],
                                              a["nb"], None, None)
 
 

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from long_context_sparse_lsa_b200 import binding as lsa
-from test_fp4_cpu import INVALID, P, UNSUPPORTED, WORKSPACE, _prompts
+from test_fp4_cpu import INVALID, P, UNSUPPORTED, WORKSPACE, _prompts, _ref
 
 
 def _prompt(**kw):
@@ -11,7 +11,7 @@ def _prompt(**kw):
              lse=P, ws=None, nb=0)
     a.update(kw)
     return lsa.load_library().lsa_attend_prompt(a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["H"], a["K"], a["d"],
-                                                a["prompts"], a["out"], a["lse"], a["ws"], a["nb"], None, None)
+                                                _ref(a["prompts"]), a["out"], a["lse"], a["ws"], a["nb"], None, None)
 
 
 few = dict(prompts=_prompts(n_seq=1, n_rows=1, max_len=9000))  # one row over a long cache: the keys are split
