@@ -445,7 +445,7 @@ lsa_status_t lsa_attend_fp8(const uint16_t *const *q, const uint8_t *const *k_ca
  *               (exact where they are bf16 normals), for attending a prompt over
  *               the same values that decoding will read.
  * Rows of two sequences that share cache rows race. All device pointers
- * 16-byte aligned (the group scales 8). Supported: d == 128; 1 <= H_kv <= 256;
+ * 16-byte aligned. Supported: d == 128; 1 <= H_kv <= 256;
  * 1 <= layers <= LSA_MAX_LAYERS; n_rows * H_kv < 2^31. One launch.
  */
 lsa_status_t lsa_store_fp4(const uint16_t *const *k_new, int64_t k_stride,

@@ -874,7 +874,7 @@ lsa_status_t lsa_store_fp4(const uint16_t* const* k_new, int64_t k_stride, const
         const void* need[] = {k_new[g], v_new[g], k[g], v[g]};
         for (const void* p : need)
             if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
-        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 8) || !aligned(v_group[g], 8))
+        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 16) || !aligned(v_group[g], 16))
             return LSA_ERR_INVALID_ARG;
         a.k_new[g] = k_new[g];
         a.v_new[g] = v_new[g];
@@ -947,7 +947,7 @@ lsa_status_t lsa_attend_fp4(const uint16_t* const* q, const uint8_t* const* k, c
         const void* need[] = {q[g], k[g], v[g], out[g]};
         for (const void* p : need)
             if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
-        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 8) || !aligned(v_group[g], 8))
+        if (k_group[g] == nullptr || v_group[g] == nullptr || !aligned(k_group[g], 16) || !aligned(v_group[g], 16))
             return LSA_ERR_INVALID_ARG;
         b.q[g] = q[g];
         b.out[g] = out[g];

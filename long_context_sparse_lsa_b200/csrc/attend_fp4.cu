@@ -7,11 +7,13 @@
 //
 // Design (B200):
 //  * grid = (splits x kv-head groups, query rows, layers). A CTA covers up to
-//    4 kv heads over one run of set entries; a warp owns one kv head and
-//    every (warps / heads)-th tile of 16 entries.
-//  * A warp gathers its own tiles with 16-byte (codes) and 8-byte (scales)
-//    asynchronous copies into a private ring of kRing tiles, so no warp
-//    waits for another and 2304 * kRing * kWarps bytes are in flight per CTA.
+//    4 kv heads over one run of set entries; a team of one warp per kv head
+//    works on every n-th step of 32 entries.
+//  * A team gathers its steps itself with 16-byte asynchronous copies into a
+//    ring of three, whole tokens at a time (the heads' codes of a token are
+//    256 consecutive bytes, their scales 32): 64 rows of 3136 random tokens
+//    take 46 us this way from HBM, 90 us when each warp fetches its own
+//    head's 64 + 8 bytes, and 60 us as one bulk copy per token.
 //  * S^T = K Q^T on fp16 tensor cores (mma.m16n8k16): 16 tokens are M, the
 //    group's query heads N. Lane (g, t) holds the 32 channels 32 t .. 32 t +
 //    31 of tokens g and g + 8 (one 16-byte read per token) and the query
@@ -41,29 +43,44 @@ namespace {
 
 constexpr int kF4Warps = 16;
 constexpr int kF4Threads = kF4Warps * kWarp;
-constexpr int kF4Tile = 16;
-constexpr int kRing = 5;
-constexpr int kF4CodeTile = kF4Tile * kFp4CodeBytes;                       // 1024: K (or V) codes of a tile
-constexpr int kF4ScaleTile = kF4Tile * kFp4Groups;                         // 128
-constexpr int kF4TileBytes = 2 * (kF4CodeTile + kF4ScaleTile);             // 2304
-constexpr int kF4RingBytes = kF4Warps * kRing * kF4TileBytes;              // 184,320
-constexpr int kF4MaxEntries = 4096;                                        // set entries per split
+constexpr int kF4Tile = 16;                                                // entries of an MMA tile
+constexpr int kF4Pair = 2 * kF4Tile;                                       // entries of one step of a warp
+constexpr int kRing = 3;                                                   // steps in a team's ring
+constexpr int kF4HeadStep = kF4Pair * 2 * (kFp4CodeBytes + kFp4Groups);    // 4608: a step of one kv head
+constexpr int kF4RingBytes = kF4Warps * kRing * kF4HeadStep;               // 221,184
 constexpr float kPBits = 10.f;                                             // P is carried as 2^10 p
-constexpr int kF4MergeFloats = (kFp4D / 16) * 4 + 4;                       // o fragments, m, l of one head tile
+constexpr int kF4Park = 36;                                                // floats of a lane: o fragments, m, l
+static_assert(kF4RingBytes <= 227 * 1024 && kF4Warps * 2 * kF4Park * kWarp * 4 <= kF4RingBytes, "shared memory of one CTA");
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes));
 }
 
-// Where MMA row m of a tile lies in the V tile: even rows 0..3, odd rows
-// 4..7 (and 8 more), with the 16-byte chunks of every second pair of rows
-// exchanged. A lane (g, t) then reads 8 bytes at chunk g / 2 of rows t or 4 +
-// t, and the 16 lanes of a half warp touch all 32 banks once.
-__device__ __forceinline__ int v_place(int m) { return (m & 8) + ((m & 1) << 2) + ((m & 7) >> 1); }
-__device__ __forceinline__ int v_chunk(int place, int chunk) { return chunk ^ (place & 2); }
+// A step in shared memory, HPC heads: K codes [32][HPC * 64 bytes], V codes
+// alike, K scales [32][HPC * 8], V scales alike. The lanes of a quarter warp
+// read 64 bytes of two K rows m, m + 1: the 64-byte blocks of the heads are
+// exchanged pairwise in every second row, so that they fall on different
+// banks. Of V a lane (g, t) reads 8 bytes at 16-byte chunk g / 2 of rows 2t
+// or 2t + 1: the rows of a tile are stored even ones first, and the chunks of
+// every second pair of rows exchanged as well, so that the 16 lanes of a half
+// warp touch all 32 banks once.
+template <int HPC>
+__device__ __forceinline__ int k_at(int m, int h, int c) {
+    return m * (HPC * kFp4CodeBytes) + 64 * (HPC > 1 ? h ^ (m & 1) : h) + 16 * c;
+}
+template <int HPC>
+__device__ __forceinline__ int v_at(int m, int h, int c) {
+    const int p = (m & 24) + ((m & 1) << 2) + ((m & 7) >> 1);
+    return p * (HPC * kFp4CodeBytes) + 64 * (HPC > 1 ? h ^ (p & 1) : h) + 16 * (c ^ (p & 2));
+}
 
-// NT: tiles of 8 query heads (H_q / H_kv up to 8 or 16).
-template <int NT>
+// NT: tiles of 8 query heads (H_q / H_kv up to 8 or 16). HPC: kv heads per CTA.
+template <int NT, int HPC>
 __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_constant__ AttendFp4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
@@ -72,7 +89,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
     const int split = blockIdx.x / b.head_groups;
     const int hgrp = blockIdx.x % b.head_groups;
     const int r = blockIdx.y, layer = blockIdx.z;
-    const int ratio = b.H_q / b.H_kv, hpc = b.hpc;
+    const int ratio = b.H_q / b.H_kv;
 
     // the caller's row metadata may be read before the wait for the preceding kernel
     const int seq = b.q_seq[r];
@@ -87,30 +104,82 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
         if (tid == 0 && blockIdx.x == 0 && layer == 0)
             flag(b.dev_status, seq < 0 || seq >= b.n_seq ? LSA_DEV_BAD_SEQ : LSA_DEV_BAD_LENGTH);
         if (split == 0) {
-            float* o = b.out[layer] + ((int64_t)r * b.H_q + hgrp * hpc * ratio) * kFp4D;
-            for (int i = tid; i < hpc * ratio * kFp4D; i += kF4Threads) o[i] = 0.f;
+            float* o = b.out[layer] + ((int64_t)r * b.H_q + hgrp * HPC * ratio) * kFp4D;
+            for (int i = tid; i < HPC * ratio * kFp4D; i += kF4Threads) o[i] = 0.f;
         }
         return;
     }
 
-    // ---- the split's entries, checked; -1 where there is none ----------------
-    int32_t* s_ent = reinterpret_cast<int32_t*>(smem + kF4RingBytes);
+    // a team of HPC warps, one per kv head, works on every n_sel-th step of 32 entries
+    constexpr int n_sel = kF4Warps / HPC;
+    const int h_local = warp % HPC, wsel = warp / HPC;
+    const int kvh = hgrp * HPC + h_local;
+    auto team_sync = [&]() {
+        if (HPC == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + wsel), "n"(HPC * kWarp) : "memory");
+    };
+
+    // ---- gather: a team's steps, kRing - 1 in flight, each warp 32 / HPC whole tokens --
+    // A lane holds one entry of a step (-1: none).
     const int e0 = split * b.entries_per_split;
     const int n_local = max(0, min(b.budget - e0, b.entries_per_split));
-    const int n_tiles = (n_local + kF4Tile - 1) / kF4Tile;
+    const int n_steps = (n_local + kF4Pair - 1) / kF4Pair;
     const int32_t* set = b.sets + (int64_t)r * b.budget + e0;
-    bool bad_entry = false;
-    for (int i = tid; i < n_tiles * kF4Tile; i += kF4Threads) {
-        int e = i < n_local ? set[i] : -1;
-        if (e < -1 || e >= L) {
-            bad_entry = true;
-            e = -1;
+    // (loaded here, checked where it is used: the check waits for the load)
+    auto entry = [&](int i) -> int {
+        const int at = i * kF4Pair + lane;
+        return i < n_steps && at < n_local ? __ldg(set + at) : -1;
+    };
+    auto checked = [&](int e) -> int {
+        if (e >= -1 && e < L) return e;
+        flag(b.dev_status, LSA_DEV_BAD_INDEX);
+        return -1;
+    };
+    constexpr int kTokens = kF4Pair / HPC, kChunks = 4 * HPC;  // tokens of a warp, 16-byte chunks of a token's codes
+    constexpr int kVCodes = HPC * kF4Pair * kFp4CodeBytes, kKScales = 2 * kVCodes, kVScales = kKScales + HPC * kF4Pair * 8;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(wsel * kRing * HPC * kF4HeadStep);
+    const uint32_t k_row = (uint32_t)(b.H_kv * kFp4CodeBytes), s_row = (uint32_t)(b.H_kv * kFp4Groups);  // bytes per token
+    const int64_t head0 = off * b.H_kv + hgrp * HPC;
+    const uint8_t* kc = a.k[layer] + head0 * kFp4CodeBytes + 16 * (lane % kChunks);
+    const uint8_t* vc = a.v[layer] + head0 * kFp4CodeBytes + 16 * (lane % kChunks);
+    // scales: HPC 4: lanes 2 i, 2 i + 1 the halves of a row; K of the warp's tokens, then V. HPC 1: a row is 8 bytes
+    constexpr int kSBytes = HPC == 1 ? 8 : 16, kSChunks = HPC * 8 / kSBytes;
+    const int s_tok = lane / kSChunks % kTokens;
+    const uint8_t* ks = a.k_group[layer] + head0 * kFp4Groups + kSBytes * (lane % kSChunks);
+    const uint8_t* vs_src = a.v_group[layer] + head0 * kFp4Groups + kSBytes * (lane % kSChunks);
+    const bool s_v = HPC > 1 && lane >= 16;
+    auto fetch = [&](int entries, uint32_t slot) {
+        const uint32_t to = ring + slot;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int m = h_local * kTokens + (32 * x + lane) / kChunks;
+            const int h = lane % kChunks >> 2, c = lane & 3;
+            const int e = __shfl_sync(0xffffffffu, entries, m);
+            const uint32_t nb = e >= 0 ? 16u : 0u;
+            const uint64_t row = (uint64_t)(uint32_t)max(e, 0) * k_row;
+            cp_async16(to + (uint32_t)k_at<HPC>(m, h, c), kc + row, nb);
+            cp_async16(to + (uint32_t)(kVCodes + v_at<HPC>(m, h, c)), vc + row, nb);
         }
-        s_ent[i] = e;
+        const int m = h_local * kTokens + s_tok;
+        const int e = __shfl_sync(0xffffffffu, entries, m);
+        const uint64_t row = (uint64_t)(uint32_t)max(e, 0) * s_row;
+        const uint32_t s_to = to + (uint32_t)(m * HPC * 8 + kSBytes * (lane % kSChunks));
+        if (HPC == 1) {
+            cp_async8(s_to + kKScales, ks + row, e >= 0 ? 8u : 0u);
+            cp_async8(s_to + kVScales, vs_src + row, e >= 0 ? 8u : 0u);
+        } else {
+            cp_async16(s_to + (s_v ? kVScales : kKScales), (s_v ? vs_src : ks) + row, e >= 0 ? 16u : 0u);
+        }
+        cp_async_commit();
+    };
+    int ent[kRing];  // entries of the steps in flight; the last is not asked for (and not checked) yet
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) ent[j] = entry(wsel + j * n_sel);
+#pragma unroll
+    for (int j = 0; j < kRing - 1; ++j) {
+        ent[j] = checked(ent[j]);
+        fetch(ent[j], (uint32_t)(j * HPC * kF4HeadStep));
     }
-    if (bad_entry) flag(b.dev_status, LSA_DEV_BAD_INDEX);
-    const int h_local = warp % hpc, wsel = warp / hpc, n_sel = kF4Warps / hpc;
-    const int kvh = hgrp * hpc + h_local;
 
     // ---- query fragments: channel order of the K lanes --------------------------
     uint32_t qb[NT][8][2];
@@ -137,7 +206,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
         int e = (int)(top >> 7) - 127;
         if (e < -126 || e > 127) e = 0;
         const float down = e >= 0 ? __uint_as_float((uint32_t)(127 - min(e, 126)) << 23) : __uint_as_float((uint32_t)(127 - e) << 23);
-        const float rest = e == 127 ? 0.5f : 1.f;
+        // (the sign of the layer's scale goes with it, so that the softmax scale is not negative)
+        const float rest = copysignf(e == 127 ? 0.5f : 1.f, b.kscale[layer]);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
@@ -149,41 +219,9 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
         for (int c = 0; c < 2; ++c) {
             const int ec = __shfl_sync(0xffffffffu, e, 4 * (2 * t4 + c));
             const bool fin = __shfl_sync(0xffffffffu, top, 4 * (2 * t4 + c)) < 0x7f80u;
-            qscale[n][c] = fin ? ldexpf(b.scale_log2 * b.kscale[layer], ec) : NAN;
+            qscale[n][c] = fin ? ldexpf(b.scale_log2 * fabsf(b.kscale[layer]), ec) : NAN;
         }
     }
-    __syncthreads();
-
-    // ---- gather: this warp's tiles, kRing in flight -------------------------------
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRing * kF4TileBytes);
-    const int64_t head = off * b.H_kv + kvh;
-    const uint8_t* kc = a.k[layer];
-    const uint8_t* vc = a.v[layer];
-    auto fetch = [&](int i, int slot) {
-        if (i < n_tiles) {
-            const uint32_t dst = ring + (uint32_t)(slot * kF4TileBytes);
-            const int32_t* ent = s_ent + i * kF4Tile;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int m = g + 8 * u;
-                const int e = ent[m];
-                const uint32_t nb = e >= 0 ? 16u : 0u;
-                const int64_t row = (head + (int64_t)max(e, 0) * b.H_kv) * kFp4CodeBytes + 16 * t4;
-                cp_async16(dst + (uint32_t)(m * kFp4CodeBytes + 16 * t4), kc + row, nb);
-                const int p = v_place(m);
-                cp_async16(dst + kF4CodeTile + (uint32_t)(p * kFp4CodeBytes + 16 * v_chunk(p, t4)), vc + row, nb);
-            }
-            const int m = lane & 15;
-            const int e = ent[m];
-            const int64_t row = (head + (int64_t)max(e, 0) * b.H_kv) * kFp4Groups;
-            cp_async8(dst + 2 * kF4CodeTile + (uint32_t)((lane >> 4) * kF4ScaleTile + m * kFp4Groups),
-                      (lane < 16 ? a.k_group[layer] : a.v_group[layer]) + row, e >= 0 ? 8u : 0u);
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int j = 0; j < kRing - 1; ++j) fetch(wsel + j * n_sel, j);
-
     float o[NT][8][4];
     float m_run[NT][2], l_run[NT][2];
 #pragma unroll
@@ -193,120 +231,145 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
         m_run[n][0] = m_run[n][1] = -INFINITY;
         l_run[n][0] = l_run[n][1] = 0.f;
     }
-    int slot = 0;
-    for (int i = wsel; i < n_tiles; i += n_sel) {
-        fetch(i + (kRing - 1) * n_sel, slot == 0 ? kRing - 1 : slot - 1);
-        cp_async_wait<kRing - 1>();
-        __syncwarp();
-        const int32_t* ent = s_ent + i * kF4Tile;
-        const bool ok_g = ent[g] >= 0, ok_g8 = ent[g + 8] >= 0;
-        const uint32_t at = ring + (uint32_t)(slot * kF4TileBytes);
-        slot = slot + 1 == kRing ? 0 : slot + 1;
-        if (!__any_sync(0xffffffffu, ok_g || ok_g8)) continue;
-        // ---- S^T: 16 tokens x 8 NT heads -------------------------------------------
-        float sacc[NT][4];
+    uint32_t slot = 0;
+    constexpr uint32_t kSlot = HPC * kF4HeadStep;
+    for (int i = wsel; i < n_steps; i += n_sel) {
+        cp_async_wait<kRing - 2>();
+        team_sync();  // the team's copies of this step have landed, and all its warps have left the step before
+        ent[kRing - 1] = checked(ent[kRing - 1]);
+        fetch(ent[kRing - 1], slot == 0 ? (kRing - 1) * kSlot : slot - kSlot);
+        const uint32_t valid = __ballot_sync(0xffffffffu, ent[0] >= 0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sacc[n][0] = sacc[n][1] = sacc[n][2] = sacc[n][3] = 0.f;
-        {
-            const uint32_t sc = at + 2 * kF4CodeTile + (uint32_t)(g * kFp4Groups + 2 * t4);
+        for (int j = 0; j < kRing - 1; ++j) ent[j] = ent[j + 1];
+        ent[kRing - 1] = entry(i + kRing * n_sel);
+        const uint32_t step = ring + slot;
+        slot = slot == (kRing - 1) * kSlot ? 0 : slot + kSlot;
+        if (valid == 0u) continue;
+        // ---- S^T: 2 x 16 tokens x 8 NT heads ------------------------------------------
+        float sacc[NT][2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t sc = step + kKScales + (uint32_t)((16 * u + g) * HPC * 8 + 8 * h_local + 2 * t4);
             uint16_t s2a, s2b;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s2a) : "r"(sc));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s2b) : "r"(sc + 8 * kFp4Groups));
-            const uint32_t ha = e4m3x2_to_half2(s2a), hb = e4m3x2_to_half2(s2b);
-            const uint4 ca = ld_shared_v4(at + (uint32_t)(g * kFp4CodeBytes + 16 * t4));
-            const uint4 cb = ld_shared_v4(at + (uint32_t)((g + 8) * kFp4CodeBytes + 16 * t4));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s2b) : "r"(sc + 8 * HPC * 8));
+            const __half2 ha = e4m3x2_to_half2(s2a), hb = e4m3x2_to_half2(s2b);
+            const uint4 ca = ld_shared_v4(step + (uint32_t)k_at<HPC>(16 * u + g, h_local, t4));
+            const uint4 cb = ld_shared_v4(step + (uint32_t)k_at<HPC>(16 * u + g + 8, h_local, t4));
             const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 // words 0, 1 are group 2 t, words 2, 3 group 2 t + 1
-                const uint32_t da = __byte_perm(ha, 0, w < 2 ? 0x1010 : 0x3232);
-                const uint32_t db = __byte_perm(hb, 0, w < 2 ? 0x1010 : 0x3232);
+                const __half2 da = w < 2 ? __low2half2(ha) : __high2half2(ha);
+                const __half2 db = w < 2 ? __low2half2(hb) : __high2half2(hb);
                 uint32_t fa[4], fb[4];
                 e2m1x8_to_f16(wa[w], fa);
                 e2m1x8_to_f16(wb[w], fb);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t fr[4] = {mul_f16x2(fa[2 * u], da), mul_f16x2(fb[2 * u], db),
-                                            mul_f16x2(fa[2 * u + 1], da), mul_f16x2(fb[2 * u + 1], db)};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16(sacc[n], fr, qb[n][2 * w + u][0], qb[n][2 * w + u][1]);
-                }
-            }
-        }
-        // ---- online softmax ------------------------------------------------------------
-        uint32_t phi[NT][2], plo[NT][2];
-        float al[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float z0 = ok_g ? sacc[n][0] * qscale[n][0] : -INFINITY;
-            const float z1 = ok_g ? sacc[n][1] * qscale[n][1] : -INFINITY;
-            const float z2 = ok_g8 ? sacc[n][2] * qscale[n][0] : -INFINITY;
-            const float z3 = ok_g8 ? sacc[n][3] * qscale[n][1] : -INFINITY;
-            float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, k));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
-            }
-            const float mn0 = fmaxf(m_run[n][0], mx0), mn1 = fmaxf(m_run[n][1], mx1);
-            const float base0 = (mn0 == -INFINITY ? 0.f : mn0) - kPBits;
-            const float base1 = (mn1 == -INFINITY ? 0.f : mn1) - kPBits;
-            al[n][0] = exp2f(m_run[n][0] - kPBits - base0);
-            al[n][1] = exp2f(m_run[n][1] - kPBits - base1);
-            const float p0 = exp2f(z0 - base0), p1 = exp2f(z1 - base1);
-            const float p2 = exp2f(z2 - base0), p3 = exp2f(z3 - base1);
-            m_run[n][0] = mn0;
-            m_run[n][1] = mn1;
-            l_run[n][0] = l_run[n][0] * al[n][0] + (p0 + p2);
-            l_run[n][1] = l_run[n][1] * al[n][1] + (p1 + p3);
-            const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
-            const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-            phi[n][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
-            phi[n][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
-            plo[n][0] = movmatrix_trans(pack_f16(p0 - f01.x, p1 - f01.y));
-            plo[n][1] = movmatrix_trans(pack_f16(p2 - f23.x, p3 - f23.y));
-        }
-        // ---- O^T += V^T P^T -----------------------------------------------------------------
-        {
-            const uint32_t vt = at + kF4CodeTile;
-            uint2 vx[4];  // tokens 2t, 2t+1, 2t+8, 2t+9: the 16 codes of group g
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int p = 8 * (j >> 1) + 4 * (j & 1) + t4;
-                vx[j] = ld_shared_v2(vt + (uint32_t)(p * kFp4CodeBytes + 16 * v_chunk(p, g >> 1) + 8 * (g & 1)));
-            }
-            uint32_t sb[4];
-            const uint32_t sc = at + 2 * kF4CodeTile + kF4ScaleTile + (uint32_t)(2 * t4 * kFp4Groups + g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[j]) : "r"(sc + (uint32_t)(((j & 1) + 8 * (j >> 1)) * kFp4Groups)));
-            const uint32_t s0 = e4m3x2_to_half2(sb[0] | (sb[1] << 8)), s8 = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t x0 = w ? vx[0].y : vx[0].x, x1 = w ? vx[1].y : vx[1].x;
-                const uint32_t x8 = w ? vx[2].y : vx[2].x, x9 = w ? vx[3].y : vx[3].x;
-                uint32_t ev[4], od[4], ev8[4], od8[4];  // even and odd channels, as token pairs
-                e2m1x8_to_f16((x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u), ev);
-                e2m1x8_to_f16(((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u), od);
-                e2m1x8_to_f16((x8 & 0x0f0f0f0fu) | ((x9 << 4) & 0xf0f0f0f0u), ev8);
-                e2m1x8_to_f16(((x8 >> 4) & 0x0f0f0f0fu) | (x9 & 0xf0f0f0f0u), od8);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t fr[4] = {mul_f16x2(ev[u], s0), mul_f16x2(od[u], s0), mul_f16x2(ev8[u], s8),
-                                            mul_f16x2(od8[u], s8)};
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t fr[4] = {mul_f16x2(fa[2 * x], da), mul_f16x2(fb[2 * x], db),
+                                            mul_f16x2(fa[2 * x + 1], da), mul_f16x2(fb[2 * x + 1], db)};
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float (&oo)[4] = o[n][4 * w + u];
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(x, fr, plo[n][0], plo[n][1]);
-                        mma_f16(x, fr, phi[n][0], phi[n][1]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) oo[c] = oo[c] * al[n][c & 1] + x[c];
+                        if (w + x == 0) mma_f16_zero(sacc[n][u], fr, qb[n][0][0], qb[n][0][1]);
+                        else mma_f16(sacc[n][u], fr, qb[n][2 * w + x][0], qb[n][2 * w + x][1]);
                     }
                 }
             }
         }
-        __syncwarp();  // the slot may be filled again
+        // ---- online softmax ------------------------------------------------------------
+        uint32_t phi[NT][2][2], plo[NT][2][2];
+        float al[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float mx[2], base[2];
+            const bool whole = valid == 0xffffffffu;
+            if (!whole) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)  // token g (c < 2) or g + 8 of tile u, head 2 t + (c & 1)
+                        if (!((valid >> (16 * u + 8 * (c >> 1) + g)) & 1u)) sacc[n][u][c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mx[c] = fmaxf(fmaxf(sacc[n][0][c], sacc[n][0][c + 2]), fmaxf(sacc[n][1][c], sacc[n][1][c + 2]));
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], k));
+                mx[c] = fmaxf(m_run[n][c], mx[c] * qscale[n][c]);  // (qscale >= 0, or NaN)
+                base[c] = mx[c] == -INFINITY ? 0.f : mx[c];
+                al[n][c] = ex2(m_run[n][c] - base[c]);
+                m_run[n][c] = mx[c];
+                base[c] -= kPBits;
+            }
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float p[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    p[c] = ex2(fmaf(sacc[n][u][c], qscale[n][c & 1], -base[c & 1]));
+                    if (!whole && sacc[n][u][c] == -INFINITY) p[c] = 0.f;  // (a scale of 0 leaves NaN)
+                    sum[c & 1] += p[c];
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const __half2 h = __floats2half2_rn(p[2 * x], p[2 * x + 1]);
+                    const float2 f = __half22float2(h);
+                    phi[n][u][x] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
+                    plo[n][u][x] = movmatrix_trans(pack_f16(p[2 * x] - f.x, p[2 * x + 1] - f.y));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) l_run[n][c] = l_run[n][c] * al[n][c] + sum[c];
+        }
+        // ---- O^T = O^T al + V^T P^T -----------------------------------------------------
+        uint2 vx[2][4];  // per tile: tokens 2t, 2t+1, 2t+8, 2t+9, the 16 codes of group g
+        __half2 vs[2][2];  // the scales of tokens 2t, 2t+1 and 2t+8, 2t+9
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                vx[u][j] = ld_shared_v2(step + kVCodes + (uint32_t)(v_at<HPC>(16 * u + 2 * t4 + (j & 1) + 8 * (j >> 1), h_local, g >> 1) + 8 * (g & 1)));
+            uint32_t sb[4];
+            const uint32_t sc = step + kVScales + (uint32_t)((16 * u + 2 * t4) * HPC * 8 + 8 * h_local + g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[j]) : "r"(sc + (uint32_t)(((j & 1) + 8 * (j >> 1)) * HPC * 8)));
+            vs[u][0] = e4m3x2_to_half2((uint16_t)(sb[0] | (sb[1] << 8)));
+            vs[u][1] = e4m3x2_to_half2((uint16_t)(sb[2] | (sb[3] << 8)));
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t ev[2][2][4], od[2][2][4];  // [tile][tokens 2t.. or 2t+8..]: even and odd channels, as token pairs
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t c0 = w ? vx[u][2 * x].y : vx[u][2 * x].x, c1 = w ? vx[u][2 * x + 1].y : vx[u][2 * x + 1].x;
+                    e2m1x8_to_f16((c0 & 0x0f0f0f0fu) | ((c1 << 4) & 0xf0f0f0f0u), ev[u][x]);
+                    e2m1x8_to_f16(((c0 >> 4) & 0x0f0f0f0fu) | (c1 & 0xf0f0f0f0u), od[u][x]);
+                }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                float acc[NT][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t fr[4] = {mul_f16x2(ev[u][0][y], vs[u][0]), mul_f16x2(od[u][0][y], vs[u][0]),
+                                            mul_f16x2(ev[u][1][y], vs[u][1]), mul_f16x2(od[u][1][y], vs[u][1])};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (u == 0) mma_f16_zero(acc[n], fr, plo[n][u][0], plo[n][u][1]);
+                        else mma_f16(acc[n], fr, plo[n][u][0], plo[n][u][1]);
+                        mma_f16(acc[n], fr, phi[n][u][0], phi[n][u][1]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][4 * w + y][c] = o[n][4 * w + y][c] * al[n][c & 1] + acc[n][c];
+            }
+        }
     }
     cp_async_wait<0>();
     pdl_trigger();
@@ -318,65 +381,65 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
             for (int k = 4; k < 32; k <<= 1) l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], k);
     __syncthreads();  // the merge area reuses the rings
 
-    // ---- merge the warps of each kv head: partners park, the first folds -----------
-    float* park = reinterpret_cast<float*>(smem);  // [warp][NT][kF4MergeFloats][32]
-    if (wsel > 0) {
+    // ---- merge the warps of each kv head: every warp parks its fragments and
+    // combines its share of the channels over the warps of the head -----------------
+    float* park = reinterpret_cast<float*>(smem);  // [warp][NT][kF4Park][32]
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float* p = park + (size_t)((warp * NT + n) * kF4MergeFloats) * kWarp + lane;
+    for (int n = 0; n < NT; ++n) {
+        float* p = park + ((warp * NT + n) * kF4Park) * kWarp + lane;
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
+        for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) p[(4 * mt + c) * kWarp] = o[n][mt][c];
-            p[32 * kWarp] = m_run[n][0];
-            p[33 * kWarp] = m_run[n][1];
-            p[34 * kWarp] = l_run[n][0];
-            p[35 * kWarp] = l_run[n][1];
+            for (int c = 0; c < 4; ++c) p[(4 * mt + c) * kWarp] = o[n][mt][c];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            p[(32 + c) * kWarp] = m_run[n][c];
+            p[(34 + c) * kWarp] = l_run[n][c];
         }
     }
     __syncthreads();
-    if (wsel > 0) return;
     const bool direct = b.n_splits == 1;
     const int64_t row_q = (int64_t)layer * b.n_q + r;
+    // the warp's share: fragment tiles [m_lo, m_lo + 8 / n_sel) of both head
+    // columns; with 16 warps a head, one tile of one column
+    constexpr int cols = n_sel == 16 ? 1 : 2, n_mt = n_sel == 16 ? 1 : 8 / n_sel;
+    const int m_lo = n_sel == 16 ? wsel >> 1 : wsel * n_mt;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        for (int j = 1; j < n_sel; ++j) {
-            const float* p = park + (size_t)(((warp + hpc * j) * NT + n) * kF4MergeFloats) * kWarp + lane;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float mb = p[(32 + c) * kWarp], lb = p[(34 + c) * kWarp];
-                const float M = fmaxf(m_run[n][c], mb);
-                const float sa = M == -INFINITY ? 0.f : exp2f(m_run[n][c] - M);
-                const float sb = M == -INFINITY ? 0.f : exp2f(mb - M);
-                m_run[n][c] = M;
-                l_run[n][c] = l_run[n][c] * sa + lb * sb;
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    o[n][mt][c] = o[n][mt][c] * sa + p[(4 * mt + c) * kWarp] * sb;
-                    o[n][mt][c + 2] = o[n][mt][c + 2] * sa + p[(4 * mt + c + 2) * kWarp] * sb;
+    for (int n = 0; n < NT; ++n)
+        for (int cc = 0; cc < cols; ++cc) {
+            const int c = n_sel == 16 ? wsel & 1 : cc;
+            const float* p0 = park + ((h_local * NT + n) * kF4Park) * kWarp + lane;
+            const int next = HPC * NT * kF4Park * kWarp;  // to the head's next warp
+            float M = -INFINITY;
+            for (int j = 0; j < n_sel; ++j) M = fmaxf(M, p0[j * next + (32 + c) * kWarp]);
+            float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+            const float base = M == -INFINITY ? 0.f : M;
+            for (int j = 0; j < n_sel; ++j) {
+                const float* p = p0 + j * next;
+                const float f = ex2(p[(32 + c) * kWarp] - base);
+                l += p[(34 + c) * kWarp] * f;
+                x[0] += p[(4 * m_lo + c) * kWarp] * f;
+                x[1] += p[(4 * m_lo + c + 2) * kWarp] * f;
+                if (n_mt == 2) {
+                    x[2] += p[(4 * m_lo + 4 + c) * kWarp] * f;
+                    x[3] += p[(4 * m_lo + 6 + c) * kWarp] * f;
                 }
             }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
             const int hh = 8 * n + 2 * t4 + c;
             if (hh >= ratio) continue;
             const int64_t qh = (int64_t)kvh * ratio + hh;
             float* dst = direct ? b.out[layer] + ((int64_t)r * b.H_q + qh) * kFp4D
                                 : b.part_o + ((row_q * b.n_splits + split) * b.H_q + qh) * kFp4D;
-            // a denominator that is not positive: no entry (0) or NaN scores (NaN stays)
-            const float inv = l_run[n][c] == 0.f ? 0.f : 1.f / l_run[n][c];
-            const float sc = direct ? inv * b.vscale[layer] : b.vscale[layer];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<float4*>(dst + kFp4Group * g + 4 * q) =
-                    make_float4(o[n][2 * q][c] * sc, o[n][2 * q][c + 2] * sc, o[n][2 * q + 1][c] * sc, o[n][2 * q + 1][c + 2] * sc);
+            // a denominator of 0: no entry (NaN scores give NaN)
+            const float to = b.vscale[layer] * (!direct ? 1.f : l == 0.f ? 0.f : 1.f / l);
+            dst += kFp4Group * g + 2 * m_lo;
+            if (n_mt == 2) *reinterpret_cast<float4*>(dst) = make_float4(x[0] * to, x[1] * to, x[2] * to, x[3] * to);
+            else *reinterpret_cast<float2*>(dst) = make_float2(x[0] * to, x[1] * to);
             // (a maximum of -infinity marks an empty partial: one of NaN scores alone is not)
-            if (!direct && g == 0)
+            if (!direct && g == 0 && m_lo == 0)
                 *reinterpret_cast<float2*>(b.part_ml + ((row_q * b.n_splits + split) * b.H_q + qh) * 2) =
-                    make_float2(l_run[n][c] == 0.f ? m_run[n][c] : fmaxf(m_run[n][c], -3e38f), l_run[n][c]);
+                    make_float2(l == 0.f ? M : fmaxf(M, -3e38f), l);
         }
-    }
 }
 
 }  // namespace
@@ -386,20 +449,18 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
     p.hpc = H_kv < 4 ? H_kv : 4;
     p.head_groups = H_kv / p.hpc;
     const long units = (long)n_q * p.head_groups * G;
-    const int tiles = (budget + kF4Tile - 1) / kF4Tile;
+    const int steps = (budget + kF4Pair - 1) / kF4Pair;
     const int n_sel = kF4Warps / p.hpc;
     int splits = units > 0 ? (int)(num_sms / units) : 1;  // one CTA per SM, one wave
-    // at least two tiles a warp: below that the merge of the splits costs more than it saves
-    const int max_splits = (tiles + 2 * n_sel - 1) / (2 * n_sel);
+    // at least two steps a warp: below that the merge of the splits costs more than it saves
+    const int max_splits = (steps + 2 * n_sel - 1) / (2 * n_sel);
     if (splits > max_splits) splits = max_splits;
-    const int min_splits = (budget + kF4MaxEntries - 1) / kF4MaxEntries;
-    if (splits < min_splits) splits = min_splits;
     if (splits < 1) splits = 1;
-    int per = (tiles + splits - 1) / splits;
+    int per = (steps + splits - 1) / splits;
     if (per < 1) per = 1;
-    p.entries_per_split = per * kF4Tile;
-    p.n_splits = tiles > 0 ? (tiles + per - 1) / per : 1;
-    p.smem_bytes = (size_t)kF4RingBytes + (size_t)p.entries_per_split * 4;
+    p.entries_per_split = per * kF4Pair;
+    p.n_splits = steps > 0 ? (steps + per - 1) / per : 1;
+    p.smem_bytes = kF4RingBytes;
     const size_t rows_q = (size_t)G * n_q;
     p.ws_bytes = 0;
     if (p.n_splits > 1) {
@@ -411,10 +472,12 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
 
 cudaError_t launch_attend_fp4(const AttendFp4Args& a, size_t smem_bytes, cudaStream_t stream) {
     const AttendArgs& b = a.base;
-    static std::atomic<uint64_t> allowed[2];
+    static std::atomic<uint64_t> allowed[6];
     const int wide = b.H_q / b.H_kv > 8;
-    auto kern = wide ? attend_fp4_kernel<2> : attend_fp4_kernel<1>;
-    cudaError_t e = allow_smem(kern, kF4RingBytes + 4 * kF4MaxEntries, allowed[wide]);
+    auto kern = b.hpc == 1 ? (wide ? attend_fp4_kernel<2, 1> : attend_fp4_kernel<1, 1>)
+                : b.hpc == 2 ? (wide ? attend_fp4_kernel<2, 2> : attend_fp4_kernel<1, 2>)
+                             : (wide ? attend_fp4_kernel<2, 4> : attend_fp4_kernel<1, 4>);
+    cudaError_t e = allow_smem(kern, kF4RingBytes, allowed[wide + 2 * (b.hpc >> 1)]);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(b.n_splits * b.head_groups), (unsigned)b.n_q, (unsigned)b.G);
     e = launch_pdl(kern, grid, dim3(kF4Threads), smem_bytes, stream, 0, a);

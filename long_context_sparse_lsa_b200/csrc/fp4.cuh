@@ -41,10 +41,11 @@ __device__ __forceinline__ uint32_t f32_to_e2m1x8(const float (&x)[8]) {
     return r;
 }
 
-// Two E4M3 bytes (bits 0..15, low first) -> an fp16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Two E4M3 bytes (low first) -> an fp16 pair (NaN stays NaN).
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint16_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+    return *reinterpret_cast<const __half2*>(&r);
 }
 
 __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
@@ -52,8 +53,8 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
     return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
