@@ -61,6 +61,10 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes));
 }
 
+__device__ __forceinline__ void cp_async_full16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+}
+
 // A step in shared memory, HPC heads: K codes [32][HPC * 64 bytes], V codes
 // alike, K scales [32][HPC * 8], V scales alike. The lanes of a quarter warp
 // read 64 bytes of two K rows m, m + 1: the 64-byte blocks of the heads are
@@ -145,30 +149,55 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
     // scales: HPC 4: lanes 2 i, 2 i + 1 the halves of a row; K of the warp's tokens, then V. HPC 1: a row is 8 bytes
     constexpr int kSBytes = HPC == 1 ? 8 : 16, kSChunks = HPC * 8 / kSBytes;
     const int s_tok = lane / kSChunks % kTokens;
-    const uint8_t* ks = a.k_group[layer] + head0 * kFp4Groups + kSBytes * (lane % kSChunks);
-    const uint8_t* vs_src = a.v_group[layer] + head0 * kFp4Groups + kSBytes * (lane % kSChunks);
-    const bool s_v = HPC > 1 && lane >= 16;
+    // (lanes 16..31 of a wider CTA take the V scales)
+    const uint8_t* sc0 = (HPC > 1 && lane >= 16 ? a.v_group[layer] : a.k_group[layer]) + head0 * kFp4Groups + kSBytes * (lane % kSChunks);
+    const uint8_t* sc1 = a.v_group[layer] + head0 * kFp4Groups;  // HPC 1
+    // lane-constant shared-memory offsets; row m = h_local * kTokens + (32 x + lane) / kChunks for x = 0..3
+    const int ch = lane % kChunks >> 2;
+    uint32_t k_off[HPC == 1 ? 1 : 4], v_off[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int m = h_local * kTokens + (32 * x + lane) / kChunks;
+        if (HPC > 1 || x == 0) k_off[x] = (uint32_t)k_at<HPC>(m, ch, lane & 3);
+        v_off[x] = (uint32_t)(kVCodes + v_at<HPC>(m, ch, lane & 3));
+    }
+    const int sm = h_local * kTokens + s_tok;
+    const uint32_t s_off = (uint32_t)((HPC > 1 && lane >= 16 ? kVScales : kKScales) + sm * HPC * 8 + kSBytes * (lane % kSChunks));
     auto fetch = [&](int entries, uint32_t slot) {
         const uint32_t to = ring + slot;
+        const bool whole = __all_sync(0xffffffffu, entries >= 0);
+        const uint32_t clamped = (uint32_t)max(entries, 0);
+        if (whole) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int m = h_local * kTokens + (32 * x + lane) / kChunks;
-            const int h = lane % kChunks >> 2, c = lane & 3;
-            const int e = __shfl_sync(0xffffffffu, entries, m);
-            const uint32_t nb = e >= 0 ? 16u : 0u;
-            const uint64_t row = (uint64_t)(uint32_t)max(e, 0) * k_row;
-            cp_async16(to + (uint32_t)k_at<HPC>(m, h, c), kc + row, nb);
-            cp_async16(to + (uint32_t)(kVCodes + v_at<HPC>(m, h, c)), vc + row, nb);
-        }
-        const int m = h_local * kTokens + s_tok;
-        const int e = __shfl_sync(0xffffffffu, entries, m);
-        const uint64_t row = (uint64_t)(uint32_t)max(e, 0) * s_row;
-        const uint32_t s_to = to + (uint32_t)(m * HPC * 8 + kSBytes * (lane % kSChunks));
-        if (HPC == 1) {
-            cp_async8(s_to + kKScales, ks + row, e >= 0 ? 8u : 0u);
-            cp_async8(s_to + kVScales, vs_src + row, e >= 0 ? 8u : 0u);
-        } else {
-            cp_async16(s_to + (s_v ? kVScales : kKScales), (s_v ? vs_src : ks) + row, e >= 0 ? 16u : 0u);
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t e = __shfl_sync(0xffffffffu, clamped, h_local * kTokens + (32 * x + lane) / kChunks);
+                cp_async_full16(to + k_off[HPC == 1 ? 0 : x] + (HPC == 1 ? (uint32_t)(8 * x * kFp4CodeBytes) : 0u), kc + (uint64_t)e * k_row);
+                cp_async_full16(to + v_off[x], vc + (uint64_t)e * k_row);
+            }
+            const uint32_t e = __shfl_sync(0xffffffffu, clamped, sm);
+            if (HPC == 1) {
+                cp_async8(to + s_off, sc0 + (uint64_t)e * s_row, 8);
+                cp_async8(to + s_off + (kVScales - kKScales), sc1 + (uint64_t)e * s_row, 8);
+            } else {
+                cp_async_full16(to + s_off, sc0 + (uint64_t)e * s_row);
+            }
+        } else {  // a missing entry's bytes are zeros
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+                const int m = h_local * kTokens + (32 * x + lane) / kChunks;
+                const uint32_t e = __shfl_sync(0xffffffffu, clamped, m);
+                const uint32_t nb = __shfl_sync(0xffffffffu, entries, m) >= 0 ? 16u : 0u;
+                cp_async16(to + (uint32_t)k_at<HPC>(m, ch, lane & 3), kc + (uint64_t)e * k_row, nb);
+                cp_async16(to + (uint32_t)(kVCodes + v_at<HPC>(m, ch, lane & 3)), vc + (uint64_t)e * k_row, nb);
+            }
+            const uint32_t e = __shfl_sync(0xffffffffu, clamped, sm);
+            const bool in = __shfl_sync(0xffffffffu, entries, sm) >= 0;
+            if (HPC == 1) {
+                cp_async8(to + s_off, sc0 + (uint64_t)e * s_row, in ? 8u : 0u);
+                cp_async8(to + s_off + (kVScales - kKScales), sc1 + (uint64_t)e * s_row, in ? 8u : 0u);
+            } else {
+                cp_async16(to + s_off, sc0 + (uint64_t)e * s_row, in ? 16u : 0u);
+            }
         }
         cp_async_commit();
     };
