@@ -995,9 +995,9 @@ static bool prompt_shape_ok(int32_t H_q, int32_t H_kv, int32_t d) {
     return d == 128 && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 64 && H_q <= 4096;
 }
 
-// Row tiles and splits as CTAs of one grid.
-static bool prompt_grid_ok(const lsa::PromptPlan& p, int32_t n_rows, int32_t H_q, int32_t H_kv) {
-    return (int64_t)p.slots * H_kv * p.n_splits <= INT32_MAX && (int64_t)n_rows * H_q <= INT32_MAX;
+// Item numbers (those of the round after the last among them) fit 32 bits.
+static bool prompt_items_ok(const lsa::PromptPlan& p, int32_t n_rows, int32_t H_q) {
+    return p.n_items <= INT32_MAX - 4096 && (int64_t)n_rows * H_q <= INT32_MAX;
 }
 
 static lsa::PromptPlan prompt_plan(const lsa_prompts_t* p, int32_t H_q, int32_t H_kv) {
@@ -1015,7 +1015,7 @@ int32_t lsa_attend_prompt_launches(const lsa_prompts_t* prompts, int32_t H_q, in
     if (prompts == nullptr || prompts->n_seq < 1 || prompts->n_rows < 1 || prompts->max_len < 1 ||
         !prompt_shape_ok(H_q, H_kv, d))
         return 0;
-    return prompt_plan(prompts, H_q, H_kv).n_splits > 1 ? 2 : 1;
+    return prompt_plan(prompts, H_q, H_kv).n_parts > 1 ? 2 : 1;
 }
 
 lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
@@ -1032,10 +1032,11 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     const void* need[] = {q, k, v, out};
     for (const void* p : need)
         if (p == nullptr || !aligned(p, 16)) return LSA_ERR_INVALID_ARG;
+    if (!aligned(out, 32)) return LSA_ERR_INVALID_ARG;
     if (lse != nullptr && !aligned(lse, 4)) return LSA_ERR_INVALID_ARG;
     const lsa::PromptPlan p = prompt_plan(prompts, H_q, H_kv);
     // tensor-map coordinates are 32-bit, strides below 2^40 bytes
-    if (!prompt_grid_ok(p, prompts->n_rows, H_q, H_kv) || prompts->total_tokens > (int64_t)INT32_MAX - 256 ||
+    if (!prompt_items_ok(p, prompts->n_rows, H_q) || prompts->total_tokens > (int64_t)INT32_MAX - 256 ||
         prompts->n_rows > INT32_MAX - 256 || q_stride >= (1ll << 38) || k_stride >= (1ll << 38) || v_stride >= (1ll << 38))
         return LSA_ERR_UNSUPPORTED;
     if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
@@ -1047,7 +1048,7 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     a.v = v;
     a.out = out;
     a.lse = lse;
-    if (p.n_splits > 1) {
+    if (p.n_parts > 1) {
         a.part_o = static_cast<float*>(workspace);
         a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.off_ml);
     }
@@ -1066,7 +1067,10 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     a.H_kv = H_kv;
     a.G = p.G;
     a.tile_tokens = p.tile_tokens;
+    a.n_items = (int32_t)p.n_items;
     a.n_splits = p.n_splits;
+    a.dual = p.dual ? 1 : 0;
+    a.n_parts = p.n_parts;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
     cudaError_t e = lsa::launch_attend_prompt(a, p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LSA_OK : cuda_fail(e);

@@ -4,31 +4,33 @@
 // one of attend.cu.
 //
 // Design (B200): S = Q K^T and O += P V on tcgen05.mma (bf16, fp32
-// accumulators in tensor memory), one CTA per work item.
+// accumulators in tensor memory), one persistent CTA per SM over a list of
+// work items (row tiles of a kv head and, for few rows, a split of the keys).
 //  * Rows: one tile of 128 rows is T = 128 / G tokens x the G query heads of
 //    one kv head, so that all of them share K and V, a short prompt fills its
 //    tiles and the causal border wastes at most one 128-key tile per T tokens.
 //    A CTA holds two such tiles (their S and O fill the 512 columns of tensor
-//    memory) over the same K/V tiles.
+//    memory): of consecutive tokens, over the same K/V tiles; or, where there
+//    are few rows, of the same tokens, over alternate K/V tiles.
 //  * Warps 0..3 and 4..7 are the softmax of the two tiles, one thread per row:
 //    scores from tensor memory, running maximum and sum in fp32, P back into
 //    the columns S came from as bf16, from where the second product reads it.
 //    While one tile's softmax runs, the tensor core works for the other.
 //  * Warp 8 loads Q and a ring of 128-key K and V tiles by TMA; one thread of
 //    warp 9 issues the MMAs; warps 10 and 11 clean V where the mask reaches it
-//    (below).
+//    (below). Every role walks the same items, so an item's loads and first
+//    products run under the end of the item before.
 //  * The output is rescaled only when a row's maximum has risen by more than
 //    2^8 over the one in use (P then stays below 2^8, sums are fp32): the
 //    softmax threads do it themselves, since S of tile j is complete only
-//    after P V of the tile before is.
+//    after P V of the tile before is (one thread issues both, in order).
 //  * Masked keys: the scores are replaced by -infinity, so P is 0, but 0 * V
 //    is not 0 where V is an infinity or NaN. In tiles that the mask reaches,
 //    V rows behind every row of the CTA (other sequences' rows, rows never
 //    written) are zeroed in shared memory, and elements that are not finite
 //    within the CTA's own tokens are zeroed and added back at the end, by each
 //    row that sees them.
-//  * Long caches and few rows: the keys are split over CTAs, whose partials
-//    prompt_merge_kernel combines by log-sum-exp.
+//  * Partials of split keys are combined by prompt_merge_kernel by log-sum-exp.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
 #include "internal.h"
@@ -42,7 +44,6 @@ constexpr int kPrRows = 128;                         // rows of a tile
 constexpr int kPrKeys = 128;                         // keys of a tile
 constexpr int kPrThreads = 384;
 constexpr int kPrStages = 5;                         // K and V tiles in the ring
-constexpr int kPrMasked = 3;                         // key tiles of a CTA that the mask may reach: it reaches fewer than 256 keys
 constexpr uint32_t kHalf = kPrRows * 128;            // 16 KB: 128 rows of 64 channels
 constexpr uint32_t kPrTile = 2 * kHalf;              // 32 KB
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // tensor-memory columns: S0, S1, O0, O1
@@ -50,16 +51,19 @@ constexpr uint32_t kIdescS = idesc_bf16(128, 128, false), kIdescO = idesc_bf16(1
 
 struct PrShared {
     uint64_t full[kPrStages], empty[kPrStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t v_raw[kPrMasked];  // a V tile that the mask reaches has landed (its `full` comes once it is clean)
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t v_raw[kPrStages];  // a V tile that the mask reaches has landed (its `full` comes once it is clean)
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
-    int32_t not_finite;
-    int32_t cleaned[kPrMasked];  // warps that are done with a V tile
+    int32_t not_finite;          // some item's own V was not all finite
+    int32_t cleaned[kPrStages];  // warps that are done with a V tile
 };
 constexpr size_t kPrSmem = 1024 + (size_t)(2 + kPrStages) * kPrTile + sizeof(PrShared);
 static_assert(kPrSmem <= 227 * 1024, "shared memory of one CTA");
+// registers per thread: the launch's 384 x 168, given to the softmax warps by the others
+constexpr int kPrRegsSoftmax = 216, kPrRegsRest = 72;
+static_assert(256 * kPrRegsSoftmax + 128 * kPrRegsRest <= kPrThreads * 168, "register split");
 
 struct PrArgs {
     CUtensorMap q, k, v;
@@ -80,6 +84,84 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// Pairs of floats in one register pair: one instruction for both.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2_down(f32x2 x, f32x2 y) {  // rounds towards -infinity
+    f32x2 r;
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// 2^x for a pair on the FMA units, beside the special-function unit's ex2 (16
+// results a clock and SM, half of what the tensor core's tiles ask for).
+// x = n + f with n = floor(x) (adding 1.5 * 2^23 rounded down leaves n in the
+// low bits), 2^f on [0, 1) by the polynomial of degree 4 with the smallest
+// largest relative error among those that are 1 at 0 (3e-6; fitted by
+// reweighted least squares), n added to the exponent. x below -127 counts as
+// -127, for which the bits are those of 0.
+__device__ __forceinline__ f32x2 ex2_poly(f32x2 x) {
+    float x0, x1;
+    unpair(x, x0, x1);
+    x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    const f32x2 big = pair(12582912.f, 12582912.f), neg = pair(-12582912.f, -12582912.f), minus = pair(-1.f, -1.f);
+    const f32x2 t = add2_down(x, big);
+    const f32x2 f = fma2(add2(t, neg), minus, x);
+    f32x2 y = fma2(f, pair(0.013426685f, 0.013426685f), pair(0.052242473f, 0.052242473f));
+    y = fma2(y, f, pair(0.2412802f, 0.2412802f));
+    y = fma2(y, f, pair(0.69304484f, 0.69304484f));
+    y = fma2(y, f, pair(1.f, 1.f));
+    float t0, t1, y0, y1;
+    unpair(t, t0, t1);
+    unpair(y, y0, y1);
+    return pair(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23)),
+                __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23)));
+}
+
+// P of 32 scores as bf16 pairs and their sum onto sum[0..1]: 2^(z c - mc).
+// Six of sixteen pairs go by the polynomial, where no score is masked.
+template <bool POLY>
+__device__ __forceinline__ void exp_row(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t (&p)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const f32x2 x = fma2(pair(z[2 * i], z[2 * i + 1]), c, neg_mc);
+        float p0, p1;
+        if (POLY && (i % 8 == 1 || i % 8 == 4 || i % 8 == 6)) {
+            const f32x2 y = ex2_poly(x);
+            sum[i & 1] = add2(sum[i & 1], y);
+            unpair(y, p0, p1);
+        } else {
+            unpair(x, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+        }
+        p[i] = pack_bf16(p0, p1);
+    }
 }
 
 // Sequence b owns the tile slots from row_offset[b] / Tc + b on: at least
@@ -107,35 +189,76 @@ __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int b) {
     return s;
 }
 
+// A work item: up to two row tiles and a range of key tiles, walked from the
+// last to the first: step s is key tile hi - 1 - s. Tile w works on the steps
+// first[w], first[w] + stride, ... below n.
+struct PrItem {
+    PrSeq sq;
+    int kvh, split;
+    int t[2];       // first token (row of the sequence) of each row tile
+    int hi, n;      // key tiles [hi - n, hi)
+    int see;        // keys that some row of the item sees
+    int masked;     // key tiles from here on hold keys that some row does not see
+    int first[2], stride;
+    bool live;
+};
+// Item i (every lane of the warp calls it). Sequences' tiles come longest first.
+__device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool report) {
+    PrItem it;
+    it.split = i % a.n_splits;
+    it.kvh = i / a.n_splits % a.H_kv;
+    const int slot = i / a.n_splits / a.H_kv;
+    const int T = a.tile_tokens, tc = a.dual ? T : 2 * T;
+    const int seq = slot_seq(a.row_offset, a.n_seq, tc, slot);
+    it.sq = pr_seq(a, seq);
+    const int local = slot - (it.sq.row0 / tc + seq);
+    const int tiles = (it.sq.n + tc - 1) / tc;
+    it.live = it.sq.n > 0 && local >= 0 && local < tiles;
+    if (it.live && !it.sq.ok) {
+        if (report && local == 0 && lane_id() == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
+        it.live = false;
+    }
+    if (!it.live) return it;
+    it.t[0] = (tiles - 1 - local) * tc;
+    it.t[1] = a.dual ? it.t[0] : it.t[0] + T;
+    const bool two = a.dual || it.t[1] < it.sq.n;
+    it.see = it.sq.base + min(it.t[0] + tc, it.sq.n);
+    it.masked = (it.sq.base + it.t[0] + 1) / kPrKeys;
+    const int nk = (it.see + kPrKeys - 1) / kPrKeys;
+    const int lo = (int)((int64_t)nk * it.split / a.n_splits);
+    it.hi = (int)((int64_t)nk * (it.split + 1) / a.n_splits);
+    it.n = it.hi - lo;
+    it.stride = a.dual ? 2 : 1;
+    if (a.dual) {
+        it.first[0] = 0;
+        it.first[1] = 1;
+    } else {
+        // the first tile may see fewer key tiles than the second
+        const int nk0 = (it.sq.base + min(it.t[0] + T, it.sq.n) + kPrKeys - 1) / kPrKeys;
+        it.first[0] = min(max(0, it.hi - nk0), it.n);
+        it.first[1] = two ? 0 : it.n;
+    }
+    return it;
+}
+
+// This CTA's items: rounds over the grid, every second one backwards, so that
+// a list that falls in size is spread evenly.
+__device__ __forceinline__ int pr_nth(int k) {
+    return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+// 32 bytes.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __grid_constant__ PrArgs args) {
     const PromptArgs& a = args.a;
     extern __shared__ __align__(16) uint8_t pr_raw[];
-    const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
-    const int split = blockIdx.x % a.n_splits;
-    const int kvh = (blockIdx.x / a.n_splits) % a.H_kv;
-    const int slot = blockIdx.x / a.n_splits / a.H_kv;
-    const int G = a.G, T = a.tile_tokens, Tc = 2 * T;
-    const int seq = slot_seq(a.row_offset, a.n_seq, Tc, slot);
-    const PrSeq sq = pr_seq(a, seq);
-    pdl_enter();
-    const int local = slot - (sq.row0 / Tc + seq);
-    const int tiles = (sq.n + Tc - 1) / Tc;
-    if (sq.n <= 0 || local < 0 || local >= tiles) return;
-    if (!sq.ok) {
-        if (tid == 0 && local == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
-        return;
-    }
-    const int t0 = (tiles - 1 - local) * Tc;  // first token (row) of the CTA; the longest first
-    // per tile: tokens [t_lo, t_hi), key tiles [0, nk); the CTA's split of the key tiles
-    const int t_end[2] = {min(t0 + T, sq.n), min(t0 + Tc, sq.n)};
-    const bool two = t0 + T < sq.n;
-    const int see = sq.base + t_end[two ? 1 : 0];  // keys that some row of the CTA sees
-    const int nk0 = (sq.base + t_end[0] + kPrKeys - 1) / kPrKeys;
-    const int nk1 = two ? (see + kPrKeys - 1) / kPrKeys : 0;
-    const int nk = max(nk0, nk1);
-    const int lo = (int)((int64_t)nk * split / a.n_splits), hi = (int)((int64_t)nk * (split + 1) / a.n_splits);
-    const int top[2] = {min(hi, nk0), min(hi, nk1)};  // tile w works on key tiles [lo, top[w])
-
+    const int tid = threadIdx.x, lane = lane_id(), warp = uniform(warp_id());
+    const int G = a.G, T = a.tile_tokens;
     const uint32_t raw = smem_u32(pr_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t sQ = base, sKV = base + 2 * kPrTile;
@@ -144,287 +267,351 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         for (int i = 0; i < kPrStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
-            }
-        for (int i = 0; i < kPrMasked; ++i) {
             mbar_init(smem_u32(&sh.v_raw[i]), 1);
             sh.cleaned[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.q_full[i]), 1);
+            mbar_init(smem_u32(&sh.q_empty[i]), 1);
             mbar_init(smem_u32(&sh.s_full[i]), 1);
             mbar_init(smem_u32(&sh.p_full[i]), 4);
             mbar_init(smem_u32(&sh.o_full[i]), 1);
         }
+        sh.not_finite = 0;
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
-        sh.not_finite = 0;
         mbar_fence_init();
     }
     if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = sh.tmem;
-    const int masked_lo = (sq.base + t0 + 1) / kPrKeys;  // key tiles from here on hold keys that some row does not see
-    const int n_it = hi - lo;
+    const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
+    pdl_enter();
 
-    if (warp == 8) {
-        // ---- TMA: Q tiles, then K and V of key tiles hi - 1 .. lo -------------------
-        if (lane == 0 && n_it > 0) {
-            for (int w = 0; w < (two ? 2 : 1); ++w) {
-                mbar_arrive_expect_tx(smem_u32(&sh.q_full[w]), (uint32_t)(T * G) * 256u);
-                for (int h = 0; h < 2; ++h)
-                    tma_load_4d(sQ + w * kPrTile + h * kHalf, &args.q, 64 * h, 0, kvh, sq.row0 + t0 + w * T,
-                                smem_u32(&sh.q_full[w]));
-            }
-            int issued = 0;
-            for (; issued < 2 * n_it; ++issued) {
-                const int st = issued % kPrStages;
-                if (issued >= kPrStages && !pr_wait(sh, sh.empty[st], ((issued / kPrStages) + 1) & 1, a.dev_status)) break;
-                if (pr_aborted(sh)) break;
-                const int j = hi - 1 - (issued >> 1);
-                const int row = (int)(sq.off + (int64_t)j * kPrKeys);
-                const uint32_t bar = (issued & 1) && j >= masked_lo ? smem_u32(&sh.v_raw[issued >> 1]) : smem_u32(&sh.full[st]);
-                mbar_arrive_expect_tx(bar, kPrTile);
-                for (int h = 0; h < 2; ++h)
-                    tma_load_3d(sKV + st * kPrTile + h * kHalf, (issued & 1) ? &args.v : &args.k, 64 * h, kvh, row, bar);
-            }
-            // every issued copy has landed before the CTA can exit
-            for (int i = issued > kPrStages ? issued - kPrStages : 0; i < issued; ++i)
-                mbar_wait_bounded(smem_u32(&sh.full[i % kPrStages]), (i / kPrStages) & 1, kWaitLimitNs);
-            for (int w = 0; w < (two ? 2 : 1); ++w) mbar_wait_bounded(smem_u32(&sh.q_full[w]), 0, kWaitLimitNs);
-        }
-    } else if (warp == 9) {
-        // ---- MMA issue ------------------------------------------------------------------
-        if (lane == 0 && n_it > 0) {
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsRest));
+        if (warp == 8) {
+            // ---- TMA: an item's Q tiles, then K and V of its key tiles --------------------
+            int loads = 0;              // K/V tiles asked for so far
+            int q_uses[2] = {0, 0};
             bool ok = true;
-            int uses[2] = {0, 0};  // S tiles issued per row tile
-            auto qk = [&](int w, int j) {
-                const int st = (2 * (hi - 1 - j)) % kPrStages;
-                const uint64_t qd = desc_k_major(sQ + w * kPrTile), kd = desc_k_major(sKV + st * kPrTile);
+            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
+                const PrItem it = pr_item(a, pr_nth(k), true);
+                if (!it.live) continue;
+                if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {  // 16 channels a step: 32 bytes on, the second half 16 KB on
-                    const uint64_t at = (uint64_t)((k & 3) * 2 + (k >> 2) * (kHalf >> 4));
-                    mma_bf16_ss(tmem + kTmemS + 128 * w, qd + at, kd + at, kIdescS, k > 0);
-                }
-                mma_commit(smem_u32(&sh.s_full[w]));
-                ++uses[w];
-            };
-            auto pv = [&](int w, int j) {
-                ok = pr_wait(sh, sh.p_full[w], (uses[w] - 1) & 1, a.dev_status);
-                if (!ok) return;
-                tmem_fence_after();
-                const int st = (2 * (hi - 1 - j) + 1) % kPrStages;
-                const uint64_t vd = desc_mn_major(sKV + st * kPrTile, kHalf);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 keys a step: 8 tensor-memory columns of P, 2048 bytes of V
-                    mma_bf16_ts(tmem + kTmemO + 128 * w, tmem + kTmemS + 128 * w + 8 * k, vd + (uint64_t)(128 * k), kIdescO,
-                                k > 0 || uses[w] > 1);
-            };
-            auto wait_v = [&](int j) {
-                const int i = 2 * (hi - 1 - j) + 1;
-                ok = pr_wait(sh, sh.full[i % kPrStages], (i / kPrStages) & 1, a.dev_status);
-            };
-            for (int w = 0; ok && w < (two ? 2 : 1); ++w) ok = pr_wait(sh, sh.q_full[w], 0, a.dev_status);
-            for (int j = hi - 1; ok && j >= lo - 1; --j) {
-                // step j: P V of key tile j + 1, then Q K^T of tile j
-                if (j >= lo) {
-                    const int i = 2 * (hi - 1 - j);
-                    ok = pr_wait(sh, sh.full[i % kPrStages], (i / kPrStages) & 1, a.dev_status);
-                    tmem_fence_after();
-                }
-                if (ok && j + 1 < hi) wait_v(j + 1);
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (j + 1 < top[w]) pv(w, j + 1);
-                    if (ok && w == 1 && j + 1 < hi) mma_commit(smem_u32(&sh.empty[(2 * (hi - 2 - j) + 1) % kPrStages]));
-                    if (ok && j >= lo && j < top[w]) qk(w, j);
-                }
-                if (ok && j >= lo) mma_commit(smem_u32(&sh.empty[(2 * (hi - 1 - j)) % kPrStages]));
-                if (pr_aborted(sh)) ok = false;
-            }
-            for (int w = 0; w < 2; ++w) mma_commit(smem_u32(&sh.o_full[w]));
-            mma_commit(smem_u32(&sh.drain));
-            mbar_wait_bounded(smem_u32(&sh.drain), 0, kWaitLimitNs);
-        }
-    } else if (warp >= 10) {
-        // ---- V under the mask -----------------------------------------------------------
-        for (int j = hi - 1; j >= max(lo, masked_lo); --j) {
-            const int i = 2 * (hi - 1 - j) + 1;
-            if (!__all_sync(0xffffffffu, pr_wait(sh, sh.v_raw[hi - 1 - j], 0, a.dev_status))) break;
-            const uint32_t v = sKV + (uint32_t)((i % kPrStages) * kPrTile);
-            // keys from the second row's own token on: some row does not see them
-            const int r_lo = max(0, sq.base + t0 + 1 - j * kPrKeys), r_end = min(kPrKeys, see - j * kPrKeys);
-            bool found = false;
-            for (int c = (warp - 10) * kWarp + lane + 8 * r_lo; c < 8 * kPrKeys; c += 2 * kWarp) {
-                const int r = c >> 3;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = v + h * kHalf + 16 * c;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    bool put = true;
-                    if (r < r_end) {
-                        x = ld_shared_v4(at);
-                        uint32_t* e = &x.x;
-                        put = false;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const bool l = (e[q] & 0x7f80u) == 0x7f80u, u = (e[q] & 0x7f800000u) == 0x7f800000u;
-                            put |= l | u;
-                            e[q] &= (l ? 0xffff0000u : 0xffffffffu) & (u ? 0x0000ffffu : 0xffffffffu);
-                        }
-                        found |= put;
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || it.first[w] >= it.n) continue;
+                        if (q_uses[w] > 0 && !pr_wait(sh, sh.q_empty[w], (q_uses[w] - 1) & 1, a.dev_status)) ok = false;
+                        ok = ok && !pr_aborted(sh);
+                        if (!ok) continue;
+                        ++q_uses[w];
+                        mbar_arrive_expect_tx(smem_u32(&sh.q_full[w]), (uint32_t)(T * G) * 256u);
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_4d(sQ + w * kPrTile + h * kHalf, &args.q, 64 * h, 0, it.kvh, it.sq.row0 + it.t[w],
+                                        smem_u32(&sh.q_full[w]));
                     }
-                    if (put)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z),
-                                     "r"(x.w)
-                                     : "memory");
+                    for (int i = 0; ok && i < 2 * it.n; ++i) {
+                        const int st = loads % kPrStages;
+                        if (loads >= kPrStages && !pr_wait(sh, sh.empty[st], (loads / kPrStages + 1) & 1, a.dev_status))
+                            ok = false;
+                        if (!ok || pr_aborted(sh)) break;
+                        const int j = it.hi - 1 - (i >> 1);
+                        const int row = (int)(it.sq.off + (int64_t)j * kPrKeys);
+                        const uint32_t bar = (i & 1) && j >= it.masked ? smem_u32(&sh.v_raw[st]) : smem_u32(&sh.full[st]);
+                        mbar_arrive_expect_tx(bar, kPrTile);
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_3d(sKV + st * kPrTile + h * kHalf, (i & 1) ? &args.v : &args.k, 64 * h, it.kvh, row, bar);
+                        ++loads;
+                    }
                 }
+                ok = __shfl_sync(0xffffffffu, (int)(ok && !pr_aborted(sh)), 0) != 0;
             }
-            if (found) sh.not_finite = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {  // the second of the two warps passes the tile on
-                __threadfence_block();
-                if (atomicAdd(&sh.cleaned[hi - 1 - j], 1) == 1) {
-                    __threadfence_block();
-                    mbar_arrive(smem_u32(&sh.full[i % kPrStages]));
+            if (lane == 0) {  // every issued copy has landed before the CTA can exit
+                for (int i = loads > kPrStages ? loads - kPrStages : 0; i < loads; ++i)
+                    mbar_wait_bounded(smem_u32(&sh.full[i % kPrStages]), (i / kPrStages) & 1, kWaitLimitNs);
+                for (int w = 0; w < 2; ++w)
+                    if (q_uses[w] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[w]), (q_uses[w] - 1) & 1, kWaitLimitNs);
+            }
+        } else if (warp == 9) {
+            // ---- MMA issue --------------------------------------------------------------------
+            const uint32_t one = elect_one();
+            int loads = 0;           // K/V tiles of the items before
+            int uses[2] = {0, 0};    // S tiles issued per row tile
+            int q_uses[2] = {0, 0};
+            bool ok = true, any = false;
+            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
+                const PrItem it = pr_item(a, pr_nth(k), false);
+                if (!it.live) continue;
+                const int n = uniform(it.n), stride = a.dual ? 2 : 1;
+                const int first[2] = {uniform(it.first[0]), uniform(it.first[1])};
+                auto wait = [&](uint64_t& bar, int parity) {
+                    ok = ok && __all_sync(0xffffffffu, pr_wait(sh, bar, (uint32_t)parity, a.dev_status));
+                };
+                if (n > 0) any = true;
+                for (int s = 0; ok && n > 0 && s < n + stride; ++s) {
+                    // step s: P V of the tile's step before, then Q K^T of step s
+                    const int p = s - stride;
+                    const int gk = loads + 2 * s, gv = loads + 2 * p + 1;  // loads of K of step s, V of step p
+                    if (s < n) wait(sh.full[gk % kPrStages], gk / kPrStages & 1);
+                    if (p >= 0) wait(sh.full[gv % kPrStages], gv / kPrStages & 1);
+                    const uint64_t kd = desc_k_major(sKV + (uint32_t)uniform(gk % kPrStages) * kPrTile);
+                    const uint64_t vd = desc_mn_major(sKV + (uint32_t)uniform(p >= 0 ? gv % kPrStages : 0) * kPrTile, kHalf);
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || (stride == 2 && (s & 1) != w)) continue;
+                        if (p >= first[w] && p < n) {
+                            wait(sh.p_full[w], (uses[w] - 1) & 1);
+                            if (!ok) continue;
+                            tmem_fence_after();
+                            const uint32_t more = p > first[w];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)  // 16 keys: 8 tensor-memory columns of P, 2048 bytes of V
+                                mma_bf16_ts(one, tmem + kTmemO + 128 * w, tmem + kTmemS + 128 * w + 8 * x, vd + (uint64_t)(128 * x),
+                                            kIdescO, x > 0 ? 1u : more);
+                            if (s >= n) mma_commit(one, smem_u32(&sh.o_full[w]));
+                        }
+                        if (s < n && s >= first[w]) {
+                            if (s == first[w]) {
+                                wait(sh.q_full[w], q_uses[w] & 1);
+                                if (!ok) continue;
+                                ++q_uses[w];
+                            }
+                            tmem_fence_after();
+                            const uint64_t qd = desc_k_major(sQ + w * kPrTile);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {  // 16 channels: 32 bytes on, the second half 16 KB on
+                                const uint64_t at = (uint64_t)((x & 3) * 2 + (x >> 2) * (kHalf >> 4));
+                                mma_bf16_ss(one, tmem + kTmemS + 128 * w, qd + at, kd + at, kIdescS, x > 0);
+                            }
+                            mma_commit(one, smem_u32(&sh.s_full[w]));
+                            if (s + stride >= n) mma_commit(one, smem_u32(&sh.q_empty[w]));
+                            ++uses[w];
+                        }
+                    }
+                    if (ok && p >= 0) mma_commit(one, smem_u32(&sh.empty[gv % kPrStages]));
+                    if (ok && s < n) mma_commit(one, smem_u32(&sh.empty[gk % kPrStages]));
+                    if (__any_sync(0xffffffffu, pr_aborted(sh))) ok = false;
                 }
+                loads = uniform(loads + 2 * n);
+            }
+            if (any) {
+                mma_commit(one, smem_u32(&sh.drain));
+                mbar_wait_bounded(smem_u32(&sh.drain), 0, kWaitLimitNs);
+            }
+        } else {
+            // ---- V under the mask ---------------------------------------------------------------
+            int loads = 0;
+            uint32_t parity = 0;  // of each stage's v_raw
+            bool ok = true;
+            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
+                const PrItem it = pr_item(a, pr_nth(k), false);
+                if (!it.live) continue;
+                for (int s = 0; s < it.n; ++s) {
+                    const int j = it.hi - 1 - s;
+                    if (j < it.masked) break;
+                    const int st = (loads + 2 * s + 1) % kPrStages;
+                    ok = __all_sync(0xffffffffu, pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status));
+                    if (!ok) break;
+                    parity ^= 1u << st;
+                    const uint32_t v = sKV + (uint32_t)(st * kPrTile);
+                    // keys behind the item's first row: some row does not see them
+                    const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = min(kPrKeys, it.see - j * kPrKeys);
+                    bool found = false;
+                    for (int c = (warp - 10) * kWarp + lane + 8 * r_lo; c < 8 * kPrKeys; c += 2 * kWarp) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t at = v + h * kHalf + 16 * c;
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            bool put = true;
+                            if ((c >> 3) < r_end) {
+                                x = ld_shared_v4(at);
+                                uint32_t* e = &x.x;
+                                put = false;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const bool l = (e[q] & 0x7f80u) == 0x7f80u, u = (e[q] & 0x7f800000u) == 0x7f800000u;
+                                    put |= l | u;
+                                    e[q] &= (l ? 0xffff0000u : 0xffffffffu) & (u ? 0x0000ffffu : 0xffffffffu);
+                                }
+                                found |= put;
+                            }
+                            if (put)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
+                                             "r"(x.z), "r"(x.w)
+                                             : "memory");
+                        }
+                    }
+                    if (found) sh.not_finite = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {  // the second of the two warps passes the tile on
+                        __threadfence_block();
+                        if (atomicAdd(&sh.cleaned[st], 1) == 1) {
+                            sh.cleaned[st] = 0;
+                            __threadfence_block();
+                            mbar_arrive(smem_u32(&sh.full[st]));
+                        }
+                    }
+                    __syncwarp();
+                }
+                loads += 2 * it.n;
             }
         }
     } else {
-        // ---- softmax: one thread per row ------------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsSoftmax));
+        // ---- softmax: one thread per row ------------------------------------------------------
         const int w = warp >> 2;
         const int r = tid & 127;
-        const int token = t0 + w * T + min(r / G, T - 1);
         const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kTmemS + 128u * w;  // lane 32 * (warp & 3) in bits 16..
         const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + 128u * w;
-        const int sees = sq.base + min(token, sq.n - 1) + 1;  // keys of this row
-        const int masked = (sq.base + t0 + w * T + 1) / kPrKeys;
         const float c = a.scale_log2;
-        float m = -INFINITY, l = 0.f;
         bool ok = true;
-        int u = 0;
-        for (int j = top[w] - 1; j >= lo; --j, ++u) {
-            ok = pr_wait(sh, sh.s_full[w], u & 1, a.dev_status) && !pr_aborted(sh);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tmem_fence_after();
-            float s[4][32];
+        int u = 0, outs = 0;  // S tiles and outputs so far
+        for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
+            const PrItem it = pr_item(a, pr_nth(k), false);
+            if (!it.live) continue;
+            const int t_w = w ? it.t[1] : it.t[0];
+            const int token = t_w + min(r / G, T - 1);
+            const int sees = it.sq.base + min(token, it.sq.n - 1) + 1;  // keys of this row
+            const int masked = (it.sq.base + t_w + 1) / kPrKeys;
+            float m = -INFINITY, l = 0.f;
+            const int first = w ? it.first[1] : it.first[0];
+            for (int s = first; s < it.n; s += it.stride, ++u) {
+                ok = __all_sync(0xffffffffu, pr_wait(sh, sh.s_full[w], u & 1, a.dev_status) && !pr_aborted(sh));
+                if (!ok) break;
+                tmem_fence_after();
+                float z[4][32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_load32(ts + 32 * q, s[q]);
+                for (int q = 0; q < 4; ++q) tmem_load32(ts + 32 * q, z[q]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_load_wait(s[q]);
-            if (j >= masked) {
-                const int lim = sees - j * kPrKeys;
+                for (int q = 0; q < 4; ++q) tmem_load_wait(z[q]);
+                const int j = it.hi - 1 - s;
+                if (j >= masked) {
+                    const int lim = sees - j * kPrKeys;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[q][i] = 32 * q + i < lim ? s[q][i] : -INFINITY;
-            }
-            float mx[4];
+                        for (int i = 0; i < 32; ++i) z[q][i] = 32 * q + i < lim ? z[q][i] : -INFINITY;
+                }
+                float mx[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                mx[q] = s[q][0];
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = fmaxf(z[q][0], z[q][1]);
 #pragma unroll
-                for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], s[q][i]);
-            }
-            const float mt = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-            // P may grow to 2^8 before the maximum in use moves
-            if (__any_sync(0xffffffffu, (mt - m) * c > 8.f)) {
-                const float al = mt == -INFINITY ? 1.f : ex2((m - mt) * c);
-                m = mt;
-                l *= al;
-                if (u > 0) {
+                    for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], z[q][i], z[q][i + 1]);
+                }
+                const float mt = fmaxf(max3(m, mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // P may grow to 2^8 before the maximum in use moves
+                if (__any_sync(0xffffffffu, (mt - m) * c > 8.f)) {
+                    const float al = mt == -INFINITY ? 1.f : ex2((m - mt) * c);
+                    m = mt;
+                    l *= al;
+                    if (s > first) {
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float o[32];
-                        tmem_load32(to + 32 * q, o);
-                        tmem_load_wait(o);
-                        uint32_t x[32];
+                        for (int q = 0; q < 8; ++q) {
+                            float o[16];
+                            tmem_load16(to + 16 * q, o);
+                            tmem_load_wait(o);
+                            uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(o[i] * al);
-                        tmem_store32(to + 32 * q, x);
+                            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[i] * al);
+                            tmem_store16(to + 16 * q, x);
+                        }
                     }
                 }
-            }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                const f32x2 c2 = pair(c, c), neg_mc = pair(-mc, -mc);
+                f32x2 sum[2] = {0, 0};
+                if (j >= masked) {
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-                uint32_t p[32];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[16];
+                        exp_row<false>(z[q], c2, neg_mc, sum, p);
+                        tmem_store16(ts + 16 * q, p);
+                    }
+                } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int qq = q + (i >> 4), e = 2 * (i & 15);
-                    const float p0 = ex2(fmaf(s[qq][e], c, -mc)), p1 = ex2(fmaf(s[qq][e + 1], c, -mc));
-                    sum[i & 3] += p0 + p1;
-                    p[i] = pack_bf16(p0, p1);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[16];
+                        exp_row<true>(z[q], c2, neg_mc, sum, p);
+                        tmem_store16(ts + 16 * q, p);
+                    }
                 }
-                tmem_store32(ts + 16 * q, p);
+                float l0, l1;
+                unpair(add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
+                tmem_store_wait();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_store_wait();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
-        }
-        // ---- output -----------------------------------------------------------------------
-        const bool live = r < T * G && token < sq.n && (w == 0 || two);
-        if (ok && u > 0) ok = pr_wait(sh, sh.o_full[w], 0, a.dev_status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && (w == 0 || two)) {
-            tmem_fence_after();
-            const int64_t row = (int64_t)sq.row0 + token;
-            const int head = kvh * G + r % G;
-            const float inv = u > 0 ? 1.f / l : 0.f;
+            if (!ok) break;
+            // ---- output -------------------------------------------------------------------------
+            const bool worked = first < it.n;
+            if (worked) {
+                ok = __all_sync(0xffffffffu, pr_wait(sh, sh.o_full[w], outs & 1, a.dev_status) && !pr_aborted(sh));
+                if (!ok) break;
+                ++outs;
+                tmem_fence_after();
+            }
+            const bool mine = r < T * G && token < it.sq.n && (worked || a.n_parts > 1);
+            const int64_t row = ((int64_t)it.sq.row0 + token) * a.H_q + it.kvh * G + r % G;
+            const int part = a.dual ? 2 * it.split + w : it.split;
+            const float inv = 1.f / l;
             const bool fix = *reinterpret_cast<volatile int32_t*>(&sh.not_finite) != 0;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                float o[32];
-                if (u > 0) {
-                    tmem_load32(to + 32 * q, o);
+            for (int q = 0; q < 8; ++q) {
+                float o[16];
+                if (worked) {
+                    tmem_load16(to + 16 * q, o);
                     tmem_load_wait(o);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
                 }
-                if (fix && live) {  // V elements of the CTA's own tokens that are not finite, where this row sees them
-                    for (int key = max(sq.base + t0 + 1, lo * kPrKeys); key < min(sees, hi * kPrKeys); ++key) {
-                        const uint16_t* vr = a.v + (sq.off + key) * a.v_stride + (int64_t)kvh * kPrD + 32 * q;
+                if (fix && mine && worked) {  // V elements of the item's own tokens that are not finite, where this row sees them
+                    for (int key = it.sq.base + it.t[0] + 1; key < sees; ++key) {
+                        const int s = it.hi - 1 - key / kPrKeys;  // the step it belongs to, if it is one of this tile's
+                        if (s < first || s >= it.n || (s - first) % it.stride != 0) continue;
+                        const uint16_t* vr = a.v + (it.sq.off + key) * a.v_stride + (int64_t)it.kvh * kPrD + 16 * q;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const float x = __uint_as_float((uint32_t)vr[i] << 16);
                             if (!isfinite(x)) o[i] += x;
                         }
                     }
                 }
-                if (live) {
-                    if (a.n_splits == 1) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H_q + head) * kPrD + 32 * q);
+                if (mine) {
+                    uint32_t x[8];
+                    if (a.n_parts == 1) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                                pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                        for (int i = 0; i < 8; ++i) x[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+                        store32(a.out + row * kPrD + 16 * q, x);
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(
-                            a.part_o + (((int64_t)split * a.n_rows + row) * a.H_q + head) * kPrD + 32 * q);
+                        float* dst = a.part_o + ((int64_t)part * a.n_rows * a.H_q + row) * kPrD + 16 * q;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[8 * h + i]);
+                            store32(dst + 8 * h, x);
+                        }
                     }
                 }
             }
-            if (live) {
-                if (a.n_splits > 1)
-                    reinterpret_cast<float2*>(a.part_ml)[((int64_t)split * a.n_rows + row) * a.H_q + head] =
+            if (mine) {
+                if (a.n_parts > 1)
+                    reinterpret_cast<float2*>(a.part_ml)[(int64_t)part * a.n_rows * a.H_q + row] =
                         make_float2(l == 0.f ? m * c : fmaxf(m * c, -3e38f), l);
                 else if (a.lse != nullptr)
-                    a.lse[row * a.H_q + head] = (m * c + log2f(l)) * 0.6931471805599453f;
+                    a.lse[row] = (m * c + log2f(l)) * 0.6931471805599453f;
             }
+            // (the next item's first P V overwrites O once P is passed on, which this warp does after these loads)
+            tmem_fence_before();
         }
     }
+    pdl_trigger();
     tmem_fence_before();
     __syncthreads();
     if (warp == 9) {
@@ -433,7 +620,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
     }
 }
 
-// One warp per (row, query head): the splits' partials by log-sum-exp.
+// One warp per (row, query head): the parts by log-sum-exp.
 constexpr int kPmWarps = 8;
 __global__ void __launch_bounds__(kPmWarps * kWarp) prompt_merge_kernel(const __grid_constant__ PromptArgs a) {
     pdl_enter();
@@ -448,19 +635,19 @@ __global__ void __launch_bounds__(kPmWarps * kWarp) prompt_merge_kernel(const __
     const int64_t step = (int64_t)a.n_rows * a.H_q;
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < a.n_splits; s0 += 8) {
+    for (int s0 = 0; s0 < a.n_parts; s0 += 8) {
         float2 ml[8];
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const bool in = s0 + u < a.n_splits;
+            const bool in = s0 + u < a.n_parts;
             ml[u] = in ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (s0 + u) * step + i) : make_float2(-INFINITY, 0.f);
             v[u] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + ((s0 + u) * step + i) * kPrD) + lane)
                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (ml[u].x == -INFINITY) continue;  // a split without keys
+            if (ml[u].x == -INFINITY) continue;  // a part without keys
             const float nm = fmaxf(M, ml[u].x);
             const float so = exp2f(M - nm), sn = exp2f(ml[u].x - nm);
             den = den * so + ml[u].y * sn;
@@ -483,17 +670,22 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     PromptPlan p;
     p.G = H_q / H_kv;
     p.tile_tokens = kPrRows / p.G;
-    p.slots = n_rows / (2 * p.tile_tokens) + n_seq;
-    // CTAs with work: each sequence with rows has at least one tile
-    const int64_t items = (int64_t)p.slots * H_kv;
     const int key_tiles = (max_len + kPrKeys - 1) / kPrKeys;
-    int64_t splits = num_sms / items;
+    // Few rows a sequence: one row tile holds them, and a CTA's second tile
+    // takes every other key tile instead of more rows.
+    p.dual = (int64_t)n_rows <= (int64_t)n_seq * p.tile_tokens && key_tiles >= 2 && (int64_t)n_seq * H_kv < num_sms;
+    const int64_t slots = n_rows / (p.dual ? p.tile_tokens : 2 * p.tile_tokens) + n_seq;
+    // sequences with rows have a slot more than tiles at most
+    int64_t splits = num_sms / (slots * H_kv);
     if (splits > key_tiles / 2) splits = key_tiles / 2;  // two key tiles a split at least
     if (splits < 1) splits = 1;
     p.n_splits = (int)splits;
+    p.n_parts = p.dual ? 2 * p.n_splits : p.n_splits;
+    p.n_items = slots * H_kv * splits;
+    p.ctas = (int)(p.n_items < num_sms ? p.n_items : num_sms);
     p.ws_bytes = 0;
-    if (p.n_splits > 1) {
-        const size_t rows = (size_t)p.n_splits * n_rows * H_q;
+    if (p.n_parts > 1) {
+        const size_t rows = (size_t)p.n_parts * n_rows * H_q;
         p.off_ml = rows * kPrD * 4;
         p.ws_bytes = (p.off_ml + rows * 8 + 255) / 256 * 256;
     }
@@ -510,9 +702,8 @@ cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaS
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(attend_prompt_kernel, kPrSmem, allowed);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_prompt_kernel, dim3((unsigned)((int64_t)p.slots * a.H_kv * p.n_splits)), dim3(kPrThreads), kPrSmem,
-                   stream, 0, args);
-    if (e != cudaSuccess || p.n_splits == 1) return e;
+    e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.ctas), dim3(kPrThreads), kPrSmem, stream, 0, args);
+    if (e != cudaSuccess || p.n_parts == 1) return e;
     const int64_t warps = (int64_t)a.n_rows * a.H_q;
     return launch_pdl(prompt_merge_kernel, dim3((unsigned)((warps + kPmWarps - 1) / kPmWarps)), dim3(kPmWarps * kWarp), 0,
                       stream, 0, a);

@@ -269,8 +269,8 @@ struct PromptArgs {
     const uint16_t* v;
     uint16_t* out;      // [n_rows][H_q][128]
     float* lse;         // [n_rows][H_q] or NULL
-    float* part_o;      // [n_splits][n_rows][H_q][128]
-    float* part_ml;     // [n_splits][n_rows][H_q][2]
+    float* part_o;      // [n_parts][n_rows][H_q][128]
+    float* part_ml;     // [n_parts][n_rows][H_q][2]
     const int32_t* row_offset;
     const int64_t* kv_offset;
     const int32_t* seq_lens;
@@ -278,11 +278,15 @@ struct PromptArgs {
     int64_t total_tokens;
     int64_t q_stride, k_stride, v_stride;
     int32_t n_seq, n_rows, max_len, H_q, H_kv;
-    int32_t G, tile_tokens, n_splits;  // query heads per kv head, tokens per row tile, key splits
+    int32_t G, tile_tokens;            // query heads per kv head, tokens per row tile
+    int32_t n_items, n_splits;         // work items, key splits of each row tile
+    int32_t dual, n_parts;             // a CTA's two tiles are of the same rows; partials per row
     float scale_log2;
 };
 struct PromptPlan {
-    int G = 1, tile_tokens = 128, slots = 0, n_splits = 1;
+    int G = 1, tile_tokens = 128, n_splits = 1, n_parts = 1, ctas = 0;
+    bool dual = false;
+    int64_t n_items = 0;
     size_t off_ml = 0, ws_bytes = 0;
 };
 PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, int num_sms);

@@ -19,7 +19,7 @@ few = dict(prompts=_prompts(n_seq=1, n_rows=1, max_len=9000))  # one row over a 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(out=None), INVALID),
-    (dict(q=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(lse=P + 2), INVALID),
+    (dict(q=P + 8), INVALID), (dict(out=P + 16), INVALID), (dict(lse=P + 2), INVALID),
     (dict(qs=4088), INVALID), (dict(ks=516), INVALID), (dict(vs=0), INVALID), (dict(ks=1 << 40), UNSUPPORTED),
     (dict(H=0), INVALID), (dict(K=0), INVALID), (dict(H=30), INVALID), (dict(d=0), INVALID), (dict(d=64), UNSUPPORTED),
     (dict(H=260, qs=1 << 16), UNSUPPORTED), (dict(H=8192, K=1024, qs=1 << 20, ks=1 << 18, vs=1 << 18), UNSUPPORTED),
