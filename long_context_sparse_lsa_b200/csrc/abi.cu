@@ -995,9 +995,9 @@ static bool prompt_shape_ok(int32_t H_q, int32_t H_kv, int32_t d) {
     return d == 128 && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 64 && H_q <= 4096;
 }
 
-// Item numbers (those of the round after the last among them) fit 32 bits.
+// One CTA per work item.
 static bool prompt_items_ok(const lsa::PromptPlan& p, int32_t n_rows, int32_t H_q) {
-    return p.n_items <= INT32_MAX - 4096 && (int64_t)n_rows * H_q <= INT32_MAX;
+    return p.n_items <= INT32_MAX && (int64_t)n_rows * H_q <= INT32_MAX;
 }
 
 static lsa::PromptPlan prompt_plan(const lsa_prompts_t* p, int32_t H_q, int32_t H_kv) {
@@ -1067,7 +1067,6 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     a.H_kv = H_kv;
     a.G = p.G;
     a.tile_tokens = p.tile_tokens;
-    a.n_items = (int32_t)p.n_items;
     a.n_splits = p.n_splits;
     a.dual = p.dual ? 1 : 0;
     a.n_parts = p.n_parts;

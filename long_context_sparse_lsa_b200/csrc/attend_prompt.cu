@@ -4,8 +4,7 @@
 // one of attend.cu.
 //
 // Design (B200): S = Q K^T and O += P V on tcgen05.mma (bf16, fp32
-// accumulators in tensor memory), one persistent CTA per SM over a list of
-// work items (row tiles of a kv head and, for few rows, a split of the keys).
+// accumulators in tensor memory), persistent CTAs over work items (row tiles of a kv head and, for few rows, a split of the keys).
 //  * Rows: one tile of 128 rows is T = 128 / G tokens x the G query heads of
 //    one kv head, so that all of them share K and V, a short prompt fills its
 //    tiles and the causal border wastes at most one 128-key tile per T tokens.
@@ -15,21 +14,24 @@
 //  * Warps 0..3 and 4..7 are the softmax of the two tiles, one thread per row:
 //    scores from tensor memory, running maximum and sum in fp32, P back into
 //    the columns S came from as bf16, from where the second product reads it.
-//    While one tile's softmax runs, the tensor core works for the other.
-//  * Warp 8 loads Q and a ring of 128-key K and V tiles by TMA; one thread of
-//    warp 9 issues the MMAs; warps 10 and 11 clean V where the mask reaches it
-//    (below). Every role walks the same items, so an item's loads and first
+//    While one tile's softmax runs, the tensor core works for the other. (Two
+//    threads per row, with half the keys each and the maximum exchanged
+//    through shared memory, were no faster: 1959 against 1929 us for a prompt
+//    of 16384 tokens, 32/4 heads.)
+//  * Warp 8 loads Q and a ring of 128-key K and V tiles by TMA; warp 9 issues
+//    the MMAs. Every role walks the same items, so an item's loads and first
 //    products run under the end of the item before.
 //  * The output is rescaled only when a row's maximum has risen by more than
-//    2^8 over the one in use (P then stays below 2^8, sums are fp32): the
-//    softmax threads do it themselves, since S of tile j is complete only
-//    after P V of the tile before is (one thread issues both, in order).
+//    2^8 over the one in use, with the next tile, or by more than 2^16, at once
+//    (P stays below 2^16, sums are fp32): the softmax threads do it themselves,
+//    since S of tile j is complete only after P V of the tile before is (one
+//    thread issues both, in order).
 //  * Masked keys: the scores are replaced by -infinity, so P is 0, but 0 * V
 //    is not 0 where V is an infinity or NaN. In tiles that the mask reaches,
 //    V rows behind every row of the CTA (other sequences' rows, rows never
 //    written) are zeroed in shared memory, and elements that are not finite
 //    within the CTA's own tokens are zeroed and added back at the end, by each
-//    row that sees them.
+//    row that sees them (the softmax warps do this while they wait for S).
 //  * Partials of split keys are combined by prompt_merge_kernel by log-sum-exp.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
@@ -42,28 +44,55 @@ namespace {
 constexpr int kPrD = 128;
 constexpr int kPrRows = 128;                         // rows of a tile
 constexpr int kPrKeys = 128;                         // keys of a tile
-constexpr int kPrThreads = 384;
+constexpr int kPrSoftmaxWarps = 8;                    // four per row tile
+constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * kWarp;  // (warps 10 and 11 only give their registers away)
 constexpr int kPrStages = 5;                         // K and V tiles in the ring
 constexpr uint32_t kHalf = kPrRows * 128;            // 16 KB: 128 rows of 64 channels
 constexpr uint32_t kPrTile = 2 * kHalf;              // 32 KB
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // tensor-memory columns: S0, S1, O0, O1
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, false), kIdescO = idesc_bf16(128, 128, true);
 
+// The sequence's rows and tokens, checked.
+struct PrSeq {
+    int row0, n, base;  // first row, rows, tokens before the first row
+    int64_t off;
+    bool ok;
+};
+// A work item: up to two row tiles and a range of key tiles, walked from the
+// last to the first: step s is key tile hi - 1 - s. Tile w works on the steps
+// first[w], first[w] + stride, ... below n.
+struct PrItem {
+    PrSeq sq;
+    int kvh, split;
+    int t[2];       // first token (row of the sequence) of each row tile
+    int hi, n;      // key tiles [hi - n, hi)
+    int see;        // keys that some row of the item sees
+    int masked;     // key tiles from here on hold keys that some row does not see
+    int first[2], stride;
+    int live;       // 1; 0: nothing to do; -1: behind the CTA's last item
+};
+constexpr int kPrItems = 3;  // items handed out ahead of their use
+
 struct PrShared {
     uint64_t full[kPrStages], empty[kPrStages];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint64_t v_raw[kPrStages];  // a V tile that the mask reaches has landed (its `full` comes once it is clean)
     uint64_t drain;
+    uint64_t answer_full;
+    alignas(16) uint32_t answer[4];        // the next item as it is won
+    uint64_t item_full[kPrItems], item_empty[kPrItems];
+    alignas(16) PrItem item[kPrItems];     // the items as warp 8 hands them out
     uint32_t tmem;
     int32_t abort;
     int32_t not_finite;          // some item's own V was not all finite
-    int32_t cleaned[kPrStages];  // warps that are done with a V tile
+    int32_t cleaned[kPrStages];  // warps that are done with a V tile under the mask
 };
-constexpr size_t kPrSmem = 1024 + (size_t)(2 + kPrStages) * kPrTile + sizeof(PrShared);
+constexpr size_t kPrSharedBytes = (sizeof(PrShared) + 1023) / 1024 * 1024;  // the tiles start on 1024 bytes
+constexpr size_t kPrSmem = kPrSharedBytes + (size_t)(2 + kPrStages) * kPrTile;
 static_assert(kPrSmem <= 227 * 1024, "shared memory of one CTA");
 // registers per thread: the launch's 384 x 168, given to the softmax warps by the others
 constexpr int kPrRegsSoftmax = 216, kPrRegsRest = 72;
-static_assert(256 * kPrRegsSoftmax + 128 * kPrRegsRest <= kPrThreads * 168, "register split");
+static_assert(32 * kPrSoftmaxWarps * kPrRegsSoftmax + 128 * kPrRegsRest <= kPrThreads * 168, "register split");
 
 struct PrArgs {
     CUtensorMap q, k, v;
@@ -85,9 +114,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The largest of three; NaN if one of them is.
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
 
@@ -117,50 +147,85 @@ __device__ __forceinline__ f32x2 add2_down(f32x2 x, f32x2 y) {  // rounds toward
     return r;
 }
 
-// 2^x for a pair on the FMA units, beside the special-function unit's ex2 (16
-// results a clock and SM, half of what the tensor core's tiles ask for).
-// x = n + f with n = floor(x) (adding 1.5 * 2^23 rounded down leaves n in the
-// low bits), 2^f on [0, 1) by the polynomial of degree 4 with the smallest
-// largest relative error among those that are 1 at 0 (3e-6; fitted by
-// reweighted least squares), n added to the exponent. x below -127 counts as
-// -127, for which the bits are those of 0.
-__device__ __forceinline__ f32x2 ex2_poly(f32x2 x) {
-    float x0, x1;
-    unpair(x, x0, x1);
-    x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-    const f32x2 big = pair(12582912.f, 12582912.f), neg = pair(-12582912.f, -12582912.f), minus = pair(-1.f, -1.f);
-    const f32x2 t = add2_down(x, big);
-    const f32x2 f = fma2(add2(t, neg), minus, x);
-    f32x2 y = fma2(f, pair(0.013426685f, 0.013426685f), pair(0.052242473f, 0.052242473f));
-    y = fma2(y, f, pair(0.2412802f, 0.2412802f));
-    y = fma2(y, f, pair(0.69304484f, 0.69304484f));
-    y = fma2(y, f, pair(1.f, 1.f));
-    float t0, t1, y0, y1;
-    unpair(t, t0, t1);
-    unpair(y, y0, y1);
-    return pair(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23)),
-                __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23)));
-}
-
-// P of 32 scores as bf16 pairs and their sum onto sum[0..1]: 2^(z c - mc).
-// Six of sixteen pairs go by the polynomial, where no score is masked.
-template <bool POLY>
-__device__ __forceinline__ void exp_row(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t (&p)[16]) {
+// P of 32 scores as bf16 pairs, and their sum onto sum[0..1]: 2^(z c - mc).
+__device__ __forceinline__ void exp_row(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t* p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const f32x2 x = fma2(pair(z[2 * i], z[2 * i + 1]), c, neg_mc);
         float p0, p1;
-        if (POLY && (i % 8 == 1 || i % 8 == 4 || i % 8 == 6)) {
-            const f32x2 y = ex2_poly(x);
-            sum[i & 1] = add2(sum[i & 1], y);
-            unpair(y, p0, p1);
-        } else {
-            unpair(x, p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-        }
+        unpair(fma2(pair(z[2 * i], z[2 * i + 1]), c, neg_mc), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
         p[i] = pack_bf16(p0, p1);
+    }
+}
+
+// The same with kPoly of the 16 pairs on the FMA units, beside the special-
+// function unit, whose 16 results a clock and SM are half of what the tensor
+// core's tiles ask for (128 columns of one warp a scheduler: 1519 cycles
+// without, 967 with 6 pairs of 16, 1217 with 8). No score is NaN.
+// 2^x: x = n + f with n = floor(x) (adding 1.5 * 2^23 rounded down leaves n in
+// the low bits), 2^f on [0, 1) by the polynomial of degree 4 with the smallest
+// largest relative error (3e-6) among those that are 1 at 0 (fitted by
+// reweighted least squares), n added to the exponent. x below -127 counts as
+// -127, for which the bits are those of 0. The pairs go through it stage by
+// stage, with a few of the others' exponentials between the stages: in
+// program order pair by pair the same takes 2021 cycles.
+constexpr int kPoly = 6;
+__device__ __forceinline__ void exp_split(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t* p) {
+    constexpr int kRest = 16 - kPoly, kStages = 7;
+    const f32x2 big = pair(12582912.f, 12582912.f), neg_big = pair(-12582912.f, -12582912.f), minus = pair(-1.f, -1.f);
+    f32x2 x[16], t[kPoly], f[kPoly], y[kPoly];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fma2(pair(z[2 * i], z[2 * i + 1]), c, neg_mc);
+    auto rest = [&](int stage) {  // the exponentials behind this stage
+#pragma unroll
+        for (int i = 0; i < kRest; ++i)
+            if (i >= kRest * (stage - 1) / kStages && i < kRest * stage / kStages) {
+                float p0, p1;
+                unpair(x[kPoly + i], p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
+                p[kPoly + i] = pack_bf16(p0, p1);
+            }
+    };
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) {
+        float x0, x1;
+        unpair(x[i], x0, x1);
+        x[i] = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    }
+    rest(1);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) t[i] = add2_down(x[i], big);
+    rest(2);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) f[i] = add2(t[i], neg_big);
+    rest(3);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) f[i] = fma2(f[i], minus, x[i]);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) y[i] = fma2(f[i], pair(0.013426685f, 0.013426685f), pair(0.052242473f, 0.052242473f));
+    rest(4);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) y[i] = fma2(y[i], f[i], pair(0.2412802f, 0.2412802f));
+    rest(5);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) y[i] = fma2(y[i], f[i], pair(0.69304484f, 0.69304484f));
+    rest(6);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) y[i] = fma2(y[i], f[i], pair(1.f, 1.f));
+    rest(7);
+#pragma unroll
+    for (int i = 0; i < kPoly; ++i) {
+        float t0, t1, y0, y1;
+        unpair(t[i], t0, t1);
+        unpair(y[i], y0, y1);
+        y0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
+        y1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
+        sum[i & 1] = add2(sum[i & 1], pair(y0, y1));
+        p[i] = pack_bf16(y0, y1);
     }
 }
 
@@ -171,12 +236,6 @@ __device__ __forceinline__ int slot_seq(const int32_t* row_offset, int n_seq, in
     return find_last(n_seq, [&](int b) { return row_offset[b] / tc + b <= slot; });
 }
 
-// The sequence's rows and tokens, checked.
-struct PrSeq {
-    int row0, n, base;  // first row, rows, tokens before the first row
-    int64_t off;
-    bool ok;
-};
 __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int b) {
     PrSeq s;
     s.row0 = a.row_offset[b];
@@ -189,19 +248,6 @@ __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int b) {
     return s;
 }
 
-// A work item: up to two row tiles and a range of key tiles, walked from the
-// last to the first: step s is key tile hi - 1 - s. Tile w works on the steps
-// first[w], first[w] + stride, ... below n.
-struct PrItem {
-    PrSeq sq;
-    int kvh, split;
-    int t[2];       // first token (row of the sequence) of each row tile
-    int hi, n;      // key tiles [hi - n, hi)
-    int see;        // keys that some row of the item sees
-    int masked;     // key tiles from here on hold keys that some row does not see
-    int first[2], stride;
-    bool live;
-};
 // Item i (every lane of the warp calls it). Sequences' tiles come longest first.
 __device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool report) {
     PrItem it;
@@ -213,10 +259,10 @@ __device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool repor
     it.sq = pr_seq(a, seq);
     const int local = slot - (it.sq.row0 / tc + seq);
     const int tiles = (it.sq.n + tc - 1) / tc;
-    it.live = it.sq.n > 0 && local >= 0 && local < tiles;
+    it.live = it.sq.n > 0 && local >= 0 && local < tiles ? 1 : 0;
     if (it.live && !it.sq.ok) {
         if (report && local == 0 && lane_id() == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
-        it.live = false;
+        it.live = 0;
     }
     if (!it.live) return it;
     it.t[0] = (tiles - 1 - local) * tc;
@@ -241,11 +287,27 @@ __device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool repor
     return it;
 }
 
-// This CTA's items: rounds over the grid, every second one backwards, so that
-// a list that falls in size is spread evenly.
-__device__ __forceinline__ int pr_nth(int k) {
-    return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-}
+// The CTA's items: the grid has one CTA per item, the first has its own index,
+// the next ones those of CTAs that had not started. Warp 8 wins them, looks
+// them up (2000 cycles of dependent loads and divisions) and hands them to the
+// other warps through a ring, ahead of their use.
+struct PrItems {
+    PrShared& sh;
+    int32_t* status;
+    int n = 0;  // items taken
+    // The next item, which stays in its place until done(); NULL: none left, or
+    // a wait gave up. The whole warp calls both.
+    __device__ __forceinline__ const PrItem* next() {
+        const bool ok = pr_wait(sh, sh.item_full[n % kPrItems], (uint32_t)(n / kPrItems) & 1u, status) && !pr_aborted(sh);
+        const PrItem* it = &sh.item[n % kPrItems];
+        return __all_sync(0xffffffffu, ok && it->live > 0) ? it : nullptr;
+    }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive(smem_u32(&sh.item_empty[n % kPrItems]));
+        ++n;
+    }
+};
 
 // 32 bytes.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
@@ -256,13 +318,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 
 __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __grid_constant__ PrArgs args) {
     const PromptArgs& a = args.a;
-    extern __shared__ __align__(16) uint8_t pr_raw[];
+    extern __shared__ __align__(1024) uint8_t pr_raw[];
     const int tid = threadIdx.x, lane = lane_id(), warp = uniform(warp_id());
     const int G = a.G, T = a.tile_tokens;
-    const uint32_t raw = smem_u32(pr_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t sQ = base, sKV = base + 2 * kPrTile;
-    PrShared& sh = *reinterpret_cast<PrShared*>(pr_raw + (base - raw) + (2 + kPrStages) * kPrTile);
+    PrShared& sh = *reinterpret_cast<PrShared*>(pr_raw);
+    const uint32_t sQ = smem_u32(pr_raw) + (uint32_t)kPrSharedBytes, sKV = sQ + 2 * kPrTile;
     if (tid == 0) {
         for (int i = 0; i < kPrStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
@@ -274,32 +334,54 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             mbar_init(smem_u32(&sh.q_full[i]), 1);
             mbar_init(smem_u32(&sh.q_empty[i]), 1);
             mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), 4);
+            mbar_init(smem_u32(&sh.p_full[i]), kPrSoftmaxWarps / 2);
             mbar_init(smem_u32(&sh.o_full[i]), 1);
         }
         sh.not_finite = 0;
+        for (int i = 0; i < kPrItems; ++i) {
+            mbar_init(smem_u32(&sh.item_full[i]), 1);
+            mbar_init(smem_u32(&sh.item_empty[i]), kPrSoftmaxWarps + 1);
+        }
+        mbar_init(smem_u32(&sh.answer_full), 1);
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         mbar_fence_init();
     }
-    if (warp == 9) tmem_alloc(smem_u32(&sh.tmem), 512);
+    if (warp == kPrSoftmaxWarps + 1) tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
     pdl_enter();
 
-    if (warp >= 8) {
+    if (warp >= kPrSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsRest));
-        if (warp == 8) {
+        if (warp == kPrSoftmaxWarps) {
             // ---- TMA: an item's Q tiles, then K and V of its key tiles --------------------
             int loads = 0;              // K/V tiles asked for so far
             int q_uses[2] = {0, 0};
+            int asked = 0, handed = 0;  // items asked for, handed out
             bool ok = true;
-            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
-                const PrItem it = pr_item(a, pr_nth(k), true);
-                if (!it.live) continue;
+            auto hand_out = [&](const PrItem& it) {
+                const int at = handed % kPrItems;
+                if (handed >= kPrItems)
+                    ok = ok && __all_sync(0xffffffffu, pr_wait(sh, sh.item_empty[at], (uint32_t)(handed / kPrItems - 1) & 1u, a.dev_status));
+                if (!ok) return;
                 if (lane == 0) {
+                    sh.item[at] = it;
+                    mbar_arrive(smem_u32(&sh.item_full[at]));
+                }
+                ++handed;
+            };
+            for (int i = (int)blockIdx.x; ok && i >= 0;) {
+                if (lane == 0) {  // the item after this one
+                    mbar_arrive_expect_tx(smem_u32(&sh.answer_full), 16);
+                    try_cancel(smem_u32(sh.answer), smem_u32(&sh.answer_full));
+                }
+                ++asked;
+                const PrItem it = pr_item(a, i, true);
+                if (it.live) hand_out(it);
+                if (lane == 0 && it.live) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         if (!ok || it.first[w] >= it.n) continue;
@@ -327,23 +409,31 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, (int)(ok && !pr_aborted(sh)), 0) != 0;
+                ok = ok && __all_sync(0xffffffffu, pr_wait(sh, sh.answer_full, (uint32_t)(asked - 1) & 1u, a.dev_status));
+                if (ok) i = cancelled_cta(smem_u32(sh.answer));
+                fence_proxy_async_smem();
+                __syncwarp();
             }
-            if (lane == 0) {  // every issued copy has landed before the CTA can exit
+            PrItem end;
+            end.live = -1;
+            hand_out(end);
+            if (lane == 0) {  // every issued copy and answer has landed before the CTA can exit
+                if (asked > 0) mbar_wait_bounded(smem_u32(&sh.answer_full), (uint32_t)(asked - 1) & 1u, kWaitLimitNs);
                 for (int i = loads > kPrStages ? loads - kPrStages : 0; i < loads; ++i)
                     mbar_wait_bounded(smem_u32(&sh.full[i % kPrStages]), (i / kPrStages) & 1, kWaitLimitNs);
                 for (int w = 0; w < 2; ++w)
                     if (q_uses[w] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[w]), (q_uses[w] - 1) & 1, kWaitLimitNs);
             }
-        } else if (warp == 9) {
+        } else if (warp == kPrSoftmaxWarps + 1) {
             // ---- MMA issue --------------------------------------------------------------------
             const uint32_t one = elect_one();
             int loads = 0;           // K/V tiles of the items before
             int uses[2] = {0, 0};    // S tiles issued per row tile
             int q_uses[2] = {0, 0};
             bool ok = true, any = false;
-            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
-                const PrItem it = pr_item(a, pr_nth(k), false);
-                if (!it.live) continue;
+            PrItems items{sh, a.dev_status};
+            for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
+                const PrItem& it = *at;
                 const int n = uniform(it.n), stride = a.dual ? 2 : 1;
                 const int first[2] = {uniform(it.first[0]), uniform(it.first[1])};
                 auto wait = [&](uint64_t& bar, int parity) {
@@ -368,8 +458,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                             const uint32_t more = p > first[w];
 #pragma unroll
                             for (int x = 0; x < 8; ++x)  // 16 keys: 8 tensor-memory columns of P, 2048 bytes of V
-                                mma_bf16_ts(one, tmem + kTmemO + 128 * w, tmem + kTmemS + 128 * w + 8 * x, vd + (uint64_t)(128 * x),
-                                            kIdescO, x > 0 ? 1u : more);
+                                mma_bf16_ts(one, tmem + kTmemO + 128 * w, tmem + kTmemS + 128 * w + 8 * x,
+                                            vd + (uint64_t)(128 * x), kIdescO, x > 0 ? 1u : more);
                             if (s >= n) mma_commit(one, smem_u32(&sh.o_full[w]));
                         }
                         if (s < n && s >= first[w]) {
@@ -395,68 +485,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                     if (__any_sync(0xffffffffu, pr_aborted(sh))) ok = false;
                 }
                 loads = uniform(loads + 2 * n);
+                items.done();
             }
             if (any) {
                 mma_commit(one, smem_u32(&sh.drain));
                 mbar_wait_bounded(smem_u32(&sh.drain), 0, kWaitLimitNs);
-            }
-        } else {
-            // ---- V under the mask ---------------------------------------------------------------
-            int loads = 0;
-            uint32_t parity = 0;  // of each stage's v_raw
-            bool ok = true;
-            for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
-                const PrItem it = pr_item(a, pr_nth(k), false);
-                if (!it.live) continue;
-                for (int s = 0; s < it.n; ++s) {
-                    const int j = it.hi - 1 - s;
-                    if (j < it.masked) break;
-                    const int st = (loads + 2 * s + 1) % kPrStages;
-                    ok = __all_sync(0xffffffffu, pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status));
-                    if (!ok) break;
-                    parity ^= 1u << st;
-                    const uint32_t v = sKV + (uint32_t)(st * kPrTile);
-                    // keys behind the item's first row: some row does not see them
-                    const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = min(kPrKeys, it.see - j * kPrKeys);
-                    bool found = false;
-                    for (int c = (warp - 10) * kWarp + lane + 8 * r_lo; c < 8 * kPrKeys; c += 2 * kWarp) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t at = v + h * kHalf + 16 * c;
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            bool put = true;
-                            if ((c >> 3) < r_end) {
-                                x = ld_shared_v4(at);
-                                uint32_t* e = &x.x;
-                                put = false;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const bool l = (e[q] & 0x7f80u) == 0x7f80u, u = (e[q] & 0x7f800000u) == 0x7f800000u;
-                                    put |= l | u;
-                                    e[q] &= (l ? 0xffff0000u : 0xffffffffu) & (u ? 0x0000ffffu : 0xffffffffu);
-                                }
-                                found |= put;
-                            }
-                            if (put)
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
-                                             "r"(x.z), "r"(x.w)
-                                             : "memory");
-                        }
-                    }
-                    if (found) sh.not_finite = 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {  // the second of the two warps passes the tile on
-                        __threadfence_block();
-                        if (atomicAdd(&sh.cleaned[st], 1) == 1) {
-                            sh.cleaned[st] = 0;
-                            __threadfence_block();
-                            mbar_arrive(smem_u32(&sh.full[st]));
-                        }
-                    }
-                    __syncwarp();
-                }
-                loads += 2 * it.n;
             }
         }
     } else {
@@ -464,30 +497,98 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         // ---- softmax: one thread per row ------------------------------------------------------
         const int w = warp >> 2;
         const int r = tid & 127;
-        const uint32_t ts = tmem + ((uint32_t)(warp & 3) << 21) + kTmemS + 128u * w;  // lane 32 * (warp & 3) in bits 16..
-        const uint32_t to = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + 128u * w;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lanes 32 * (warp & 3) on, in bits 16..
+        const uint32_t ts = tmem + lanes + kTmemS + 128u * w, to = tmem + lanes + kTmemO + 128u * w;
         const float c = a.scale_log2;
+        const f32x2 c2 = pair(c, c);
         bool ok = true;
         int u = 0, outs = 0;  // S tiles and outputs so far
-        for (int k = 0; ok && pr_nth(k) < a.n_items; ++k) {
-            const PrItem it = pr_item(a, pr_nth(k), false);
-            if (!it.live) continue;
+        int loads = 0;        // K/V tiles of the items before
+        uint32_t parity = 0;  // of each stage's v_raw
+        // V of key tile j under the mask, by the four warps of a tile: rows behind
+        // `see` become zeros, elements that are not finite are zeroed and noted.
+        auto clean = [&](const PrItem& it, int j, int st) {
+            if (!pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status)) return;
+            const uint32_t v = sKV + (uint32_t)(st * kPrTile);
+            // keys behind the item's first row: some row does not see them
+            const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = min(kPrKeys, it.see - j * kPrKeys);
+            bool found = false;
+            for (int i = r + 8 * r_lo; i < 8 * kPrKeys; i += 128) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = v + h * kHalf + 16 * i;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    bool put = true;
+                    if ((i >> 3) < r_end) {
+                        x = ld_shared_v4(at);
+                        uint32_t* e = &x.x;
+                        put = false;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const bool lo = (e[q] & 0x7f80u) == 0x7f80u, up = (e[q] & 0x7f800000u) == 0x7f800000u;
+                            put |= lo | up;
+                            e[q] &= (lo ? 0xffff0000u : 0xffffffffu) & (up ? 0x0000ffffu : 0xffffffffu);
+                        }
+                        found |= put;
+                    }
+                    if (put)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                                     : "memory");
+                }
+            }
+            if (found) sh.not_finite = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {  // the last of the four warps passes the tile on
+                __threadfence_block();
+                if (atomicAdd(&sh.cleaned[st], 1) == 3) {
+                    sh.cleaned[st] = 0;
+                    __threadfence_block();
+                    mbar_arrive(smem_u32(&sh.full[st]));
+                }
+            }
+            __syncwarp();
+        };
+        PrItems items{sh, a.dev_status};
+        for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
+            const PrItem& it = *at;
             const int t_w = w ? it.t[1] : it.t[0];
             const int token = t_w + min(r / G, T - 1);
             const int sees = it.sq.base + min(token, it.sq.n - 1) + 1;  // keys of this row
             const int masked = (it.sq.base + t_w + 1) / kPrKeys;
             float m = -INFINITY, l = 0.f;
             const int first = w ? it.first[1] : it.first[0];
+            bool pending = false;  // the maximum in use moves to m_next with the next tile
+            float m_next = m;
+            auto move_max = [&](float to_m, bool scale_o) {
+                const float al = to_m == -INFINITY ? 1.f : ex2((m - to_m) * c);
+                m = to_m;
+                l *= al;
+                if (!scale_o) return;
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                    float o[16];
+                    tmem_load16(to + 16 * q, o);
+                    tmem_load_wait(o);
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[i] * al);
+                    tmem_store16(to + 16 * q, x);
+                }
+            };
             for (int s = first; s < it.n; s += it.stride, ++u) {
+                const int j = it.hi - 1 - s;
+                if (j >= it.masked && (w == 0 || a.dual || s < it.first[0])) clean(it, j, (loads + 2 * s + 1) % kPrStages);
                 ok = __all_sync(0xffffffffu, pr_wait(sh, sh.s_full[w], u & 1, a.dev_status) && !pr_aborted(sh));
                 if (!ok) break;
                 tmem_fence_after();
+                if (pending) move_max(m_next, true);
+                pending = false;
                 float z[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_load32(ts + 32 * q, z[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_load_wait(z[q]);
-                const int j = it.hi - 1 - s;
                 if (j >= masked) {
                     const int lim = sees - j * kPrKeys;
 #pragma unroll
@@ -498,44 +599,38 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 float mx[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    mx[q] = fmaxf(z[q][0], z[q][1]);
+                    mx[q] = max3(z[q][0], z[q][1], z[q][2]);
 #pragma unroll
-                    for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], z[q][i], z[q][i + 1]);
+                    for (int i = 3; i < 31; i += 2) mx[q] = max3(mx[q], z[q][i], z[q][i + 1]);
+                    mx[q] = max3(mx[q], mx[q], z[q][31]);
                 }
-                const float mt = fmaxf(max3(m, mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                // P may grow to 2^8 before the maximum in use moves
-                if (__any_sync(0xffffffffu, (mt - m) * c > 8.f)) {
-                    const float al = mt == -INFINITY ? 1.f : ex2((m - mt) * c);
-                    m = mt;
-                    l *= al;
-                    if (s > first) {
-#pragma unroll 1
-                        for (int q = 0; q < 8; ++q) {
-                            float o[16];
-                            tmem_load16(to + 16 * q, o);
-                            tmem_load_wait(o);
-                            uint32_t x[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[i] * al);
-                            tmem_store16(to + 16 * q, x);
-                        }
-                    }
+                // (rows behind the tile's last hold anything and have no say)
+                const float mt = r < T * G ? max3(max3(m, mx[0], mx[1]), mx[2], mx[3]) : 0.f;
+                const float rise = (mt - m) * c;
+                // Behind the first tile the maximum in use stays for this one,
+                // unless it has risen far.
+                const bool nan = __any_sync(0xffffffffu, mt != mt);
+                const bool now = s == first || nan || __any_sync(0xffffffffu, rise > 16.f);
+                if (__any_sync(0xffffffffu, !(rise <= 8.f))) {
+                    pending = !now;
+                    m_next = mt;
+                    if (now) move_max(mt, s > first);
                 }
                 const float mc = m == -INFINITY ? 0.f : m * c;
-                const f32x2 c2 = pair(c, c), neg_mc = pair(-mc, -mc);
+                const f32x2 neg_mc = pair(-mc, -mc);
                 f32x2 sum[2] = {0, 0};
-                if (j >= masked) {
+                if (!nan) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t p[16];
-                        exp_row<false>(z[q], c2, neg_mc, sum, p);
+                        exp_split(z[q], c2, neg_mc, sum, p);
                         tmem_store16(ts + 16 * q, p);
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t p[16];
-                        exp_row<true>(z[q], c2, neg_mc, sum, p);
+                        exp_row(z[q], c2, neg_mc, sum, p);
                         tmem_store16(ts + 16 * q, p);
                     }
                 }
@@ -548,6 +643,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
             }
             if (!ok) break;
+            for (int s = 0; s < it.n && it.hi - 1 - s >= it.masked; ++s) parity ^= 1u << (loads + 2 * s + 1) % kPrStages;
+            loads += 2 * it.n;
             // ---- output -------------------------------------------------------------------------
             const bool worked = first < it.n;
             if (worked) {
@@ -560,61 +657,64 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             const int64_t row = ((int64_t)it.sq.row0 + token) * a.H_q + it.kvh * G + r % G;
             const int part = a.dual ? 2 * it.split + w : it.split;
             const float inv = 1.f / l;
-            const bool fix = *reinterpret_cast<volatile int32_t*>(&sh.not_finite) != 0;
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-                float o[16];
-                if (worked) {
-                    tmem_load16(to + 16 * q, o);
-                    tmem_load_wait(o);
-                } else {
+            float o[4][32];
+            if (worked) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                }
-                if (fix && mine && worked) {  // V elements of the item's own tokens that are not finite, where this row sees them
-                    for (int key = it.sq.base + it.t[0] + 1; key < sees; ++key) {
-                        const int s = it.hi - 1 - key / kPrKeys;  // the step it belongs to, if it is one of this tile's
-                        if (s < first || s >= it.n || (s - first) % it.stride != 0) continue;
-                        const uint16_t* vr = a.v + (it.sq.off + key) * a.v_stride + (int64_t)it.kvh * kPrD + 16 * q;
+                for (int q = 0; q < 4; ++q) tmem_load32(to + 32 * q, o[q]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = __uint_as_float((uint32_t)vr[i] << 16);
-                            if (!isfinite(x)) o[i] += x;
+                for (int q = 0; q < 4; ++q) tmem_load_wait(o[q]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[q][i] = 0.f;
+            }
+            if (*reinterpret_cast<volatile int32_t*>(&sh.not_finite) != 0 && mine && worked) {
+                // V elements of the item's own tokens that are not finite, where this row sees them
+                for (int key = it.sq.base + it.t[0] + 1; key < sees; ++key) {
+                    const int s = it.hi - 1 - key / kPrKeys;  // the step it belongs to, if it is one of this tile's
+                    if (s < first || s >= it.n || (s - first) % it.stride != 0) continue;
+                    const uint16_t* vr = a.v + (it.sq.off + key) * a.v_stride + (int64_t)it.kvh * kPrD;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x = __uint_as_float((uint32_t)vr[32 * q + i] << 16);
+                            if (!isfinite(x)) o[q][i] += x;
                         }
-                    }
-                }
-                if (mine) {
-                    uint32_t x[8];
-                    if (a.n_parts == 1) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-                        store32(a.out + row * kPrD + 16 * q, x);
-                    } else {
-                        float* dst = a.part_o + ((int64_t)part * a.n_rows * a.H_q + row) * kPrD + 16 * q;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[8 * h + i]);
-                            store32(dst + 8 * h, x);
-                        }
-                    }
                 }
             }
             if (mine) {
-                if (a.n_parts > 1)
-                    reinterpret_cast<float2*>(a.part_ml)[(int64_t)part * a.n_rows * a.H_q + row] =
-                        make_float2(l == 0.f ? m * c : fmaxf(m * c, -3e38f), l);
-                else if (a.lse != nullptr)
-                    a.lse[row] = (m * c + log2f(l)) * 0.6931471805599453f;
+                uint32_t x[8];
+                if (a.n_parts == 1) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = pack_bf16(o[q >> 1][16 * (q & 1) + 2 * i] * inv, o[q >> 1][16 * (q & 1) + 2 * i + 1] * inv);
+                        store32(a.out + row * kPrD + 16 * q, x);
+                    }
+                    if (a.lse != nullptr) a.lse[row] = (m * c + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    const int64_t at = (int64_t)part * a.n_rows * a.H_q + row;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[q >> 2][8 * (q & 3) + i]);
+                        store32(a.part_o + at * kPrD + 8 * q, x);
+                    }
+                    reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(l == 0.f ? m * c : fmaxf(m * c, -3e38f), l);
+                }
             }
             // (the next item's first P V overwrites O once P is passed on, which this warp does after these loads)
             tmem_fence_before();
+            items.done();
         }
     }
     pdl_trigger();
     tmem_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kPrSoftmaxWarps + 1) {
         tmem_fence_after();
         tmem_free(tmem, 512);
     }
@@ -674,15 +774,30 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     // Few rows a sequence: one row tile holds them, and a CTA's second tile
     // takes every other key tile instead of more rows.
     p.dual = (int64_t)n_rows <= (int64_t)n_seq * p.tile_tokens && key_tiles >= 2 && (int64_t)n_seq * H_kv < num_sms;
-    const int64_t slots = n_rows / (p.dual ? p.tile_tokens : 2 * p.tile_tokens) + n_seq;
-    // sequences with rows have a slot more than tiles at most
-    int64_t splits = num_sms / (slots * H_kv);
-    if (splits > key_tiles / 2) splits = key_tiles / 2;  // two key tiles a split at least
-    if (splits < 1) splits = 1;
-    p.n_splits = (int)splits;
+    // (sequences with rows have a slot more than tiles at most)
+    const int tc = p.dual ? p.tile_tokens : 2 * p.tile_tokens;
+    const int64_t slots = n_rows / tc + n_seq;
+    const int64_t items = (((int64_t)n_rows + tc - 1) / tc + (n_seq - 1) / 2) * H_kv;  // about those with rows
+    // Key splits: as many as give the shortest of (rounds of items over the
+    // SMs) x (key tiles of an item, with its start and end) + the merge, in us:
+    // a step of both tiles takes about 1.7, an item's start and end 5, a row's
+    // partials are written and read at about 4 TB/s.
+    const int64_t keys = max_len - (n_rows / n_seq) / 2 > kPrKeys ? max_len - (n_rows / n_seq) / 2 : kPrKeys;
+    const double steps = (double)((keys + kPrKeys - 1) / kPrKeys) / (p.dual ? 2 : 1);
+    double best = 0;
+    p.n_splits = 1;
+    for (int s = 1; s <= 64 && s <= key_tiles; ++s) {
+        const int64_t rounds = (items * s + num_sms - 1) / num_sms;
+        const int parts = p.dual ? 2 * s : s;
+        const double merge = parts > 1 ? 3 + 2.0 * parts * n_rows * H_q * 520 / 4e6 : 0;
+        const double t = (double)rounds * (1.7 * (double)((int64_t)(steps / s) + 1) + 5) + merge;
+        if (s == 1 || t < 0.97 * best) {
+            best = t;
+            p.n_splits = s;
+        }
+    }
     p.n_parts = p.dual ? 2 * p.n_splits : p.n_splits;
-    p.n_items = slots * H_kv * splits;
-    p.ctas = (int)(p.n_items < num_sms ? p.n_items : num_sms);
+    p.n_items = slots * H_kv * p.n_splits;
     p.ws_bytes = 0;
     if (p.n_parts > 1) {
         const size_t rows = (size_t)p.n_parts * n_rows * H_q;
@@ -702,7 +817,7 @@ cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaS
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(attend_prompt_kernel, kPrSmem, allowed);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.ctas), dim3(kPrThreads), kPrSmem, stream, 0, args);
+    e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.n_items), dim3(kPrThreads), kPrSmem, stream, 0, args);
     if (e != cudaSuccess || p.n_parts == 1) return e;
     const int64_t warps = (int64_t)a.n_rows * a.H_q;
     return launch_pdl(prompt_merge_kernel, dim3((unsigned)((warps + kPmWarps - 1) / kPmWarps)), dim3(kPmWarps * kWarp), 0,

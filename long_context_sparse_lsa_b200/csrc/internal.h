@@ -279,12 +279,12 @@ struct PromptArgs {
     int64_t q_stride, k_stride, v_stride;
     int32_t n_seq, n_rows, max_len, H_q, H_kv;
     int32_t G, tile_tokens;            // query heads per kv head, tokens per row tile
-    int32_t n_items, n_splits;         // work items, key splits of each row tile
+    int32_t n_splits;                  // key splits of each row tile
     int32_t dual, n_parts;             // a CTA's two tiles are of the same rows; partials per row
     float scale_log2;
 };
 struct PromptPlan {
-    int G = 1, tile_tokens = 128, n_splits = 1, n_parts = 1, ctas = 0;
+    int G = 1, tile_tokens = 128, n_splits = 1, n_parts = 1;
     bool dual = false;
     int64_t n_items = 0;
     size_t off_ml = 0, ws_bytes = 0;

@@ -125,6 +125,29 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Work stealing: asks for a CTA of this grid that has not started (16 bytes at
+// `answer`, completing on the mbarrier, which expects them), and reads the
+// answer: its index along x, or -1 when none was left. After a -1 the CTA must
+// not ask again.
+__device__ __forceinline__ void try_cancel(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int cancelled_cta(uint32_t answer) {
+    uint32_t x = 0, got;
+    asm volatile(
+        "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %1, 1, 0, p;\n"
+        " mov.u32 %0, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}\n"
+        : "=r"(x), "=r"(got)
+        : "r"(answer)
+        : "memory");
+    return got ? (int)x : -1;
+}
+
 // Tensor-map tile loads into shared memory, completing their bytes on the
 // mbarrier. No multicast. x (the innermost coordinate, in elements) times the
 // element size must be a multiple of 16 bytes.
