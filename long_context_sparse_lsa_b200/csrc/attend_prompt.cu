@@ -147,23 +147,10 @@ __device__ __forceinline__ f32x2 add2_down(f32x2 x, f32x2 y) {  // rounds toward
     return r;
 }
 
-// P of 32 scores as bf16 pairs, and their sum onto sum[0..1]: 2^(z c - mc).
-__device__ __forceinline__ void exp_row(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t* p) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float p0, p1;
-        unpair(fma2(pair(z[2 * i], z[2 * i + 1]), c, neg_mc), p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        sum[i & 1] = add2(sum[i & 1], pair(p0, p1));
-        p[i] = pack_bf16(p0, p1);
-    }
-}
-
-// The same with kPoly of the 16 pairs on the FMA units, beside the special-
-// function unit, whose 16 results a clock and SM are half of what the tensor
+// P of 32 scores as bf16 pairs, and their sum onto sum[0..1]: 2^(z c - mc),
+// kPoly of the 16 pairs on the FMA units, beside the special-function unit, whose 16 results a clock and SM are half of what the tensor
 // core's tiles ask for (128 columns of one warp a scheduler: 1519 cycles
-// without, 967 with 6 pairs of 16, 1217 with 8). No score is NaN.
+// without, 967 with 6 pairs of 16, 1217 with 8). A NaN may come out as a number.
 // 2^x: x = n + f with n = floor(x) (adding 1.5 * 2^23 rounded down leaves n in
 // the low bits), 2^f on [0, 1) by the polynomial of degree 4 with the smallest
 // largest relative error (3e-6) among those that are 1 at 0 (fitted by
@@ -609,14 +596,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                     for (int i = 3; i < 31; i += 2) mx[q] = max3(mx[q], z[q][i], z[q][i + 1]);
                     mx[q] = max3(mx[q], mx[q], z[q][31]);
                 }
-                // (rows behind the tile's last hold anything and have no say)
-                const float mt = r < T * G ? max3(max3(m, mx[0], mx[1]), mx[2], mx[3]) : 0.f;
+                const float top = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
+                // A score that is NaN makes the row NaN, by its sum. (Rows behind the
+                // tile's last hold anything and have no say.)
+                if (top != top) l = NAN;
+                const float mt = top == top && r < T * G ? top : m;
                 const float rise = (mt - m) * c;
                 // Behind the first tile the maximum in use stays for this one,
                 // unless it has risen far.
-                const bool nan = __any_sync(0xffffffffu, mt != mt);
-                const bool now = s == first || nan || __any_sync(0xffffffffu, rise > 16.f);
-                if (__any_sync(0xffffffffu, !(rise <= 8.f))) {
+                const bool now = s == first || __any_sync(0xffffffffu, rise > 16.f);
+                if (__any_sync(0xffffffffu, rise > 8.f)) {
                     pending = !now;
                     m_next = mt;
                     if (now) move_max(mt, s > first);
@@ -624,20 +613,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 const float mc = m == -INFINITY ? 0.f : m * c;
                 const f32x2 neg_mc = pair(-mc, -mc);
                 f32x2 sum[2] = {0, 0};
-                if (!nan) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t p[16];
-                        exp_split(z[q], c2, neg_mc, sum, p);
-                        tmem_store16(ts + 16 * q, p);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t p[16];
-                        exp_row(z[q], c2, neg_mc, sum, p);
-                        tmem_store16(ts + 16 * q, p);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[16];
+                    exp_split(z[q], c2, neg_mc, sum, p);
+                    tmem_store16(ts + 16 * q, p);
                 }
                 float l0, l1;
                 unpair(add2(sum[0], sum[1]), l0, l1);
