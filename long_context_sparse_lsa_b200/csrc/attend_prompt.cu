@@ -19,8 +19,7 @@
 //    through shared memory, were no faster: 1959 against 1929 us for a prompt
 //    of 16384 tokens, 32/4 heads.)
 //  * Warp 8 loads Q and a ring of 128-key K and V tiles by TMA; warp 9 issues
-//    the MMAs; warp 10 wins and hands out the items; warp 11 looks after V
-//    under the mask (below). Every role walks the same items, so an item's loads and first
+//    the MMAs. Every role walks the same items, so an item's loads and first
 //    products run under the end of the item before.
 //  * The output is rescaled only when a row's maximum has risen by more than
 //    2^8 over the one in use, with the next tile, or by more than 2^16, at once
@@ -28,11 +27,11 @@
 //    since S of tile j is complete only after P V of the tile before is (one
 //    thread issues both, in order).
 //  * Masked keys: the scores are replaced by -infinity, so P is 0, but 0 * V
-//    is not 0 where V is an infinity or NaN. In the (one to three) tiles that
-//    the mask reaches, elements of V behind the item's first row's token that
-//    are not finite are zeroed in shared memory before the product; those of
-//    the item's own tokens are added back at the end, by each row that sees
-//    them. (Done by the softmax warps it cost 2500 cycles an item.)
+//    is not 0 where V is an infinity or NaN. In tiles that the mask reaches,
+//    V rows behind every row of the CTA (other sequences' rows, rows never
+//    written) are zeroed in shared memory, and elements that are not finite
+//    within the CTA's own tokens are zeroed and added back at the end, by each
+//    row that sees them (the softmax warps do this while they wait for S).
 //  * Partials of split keys are combined by prompt_merge_kernel by log-sum-exp.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
@@ -46,7 +45,7 @@ constexpr int kPrD = 128;
 constexpr int kPrRows = 128;                         // rows of a tile
 constexpr int kPrKeys = 128;                         // keys of a tile
 constexpr int kPrSoftmaxWarps = 8;                    // four per row tile
-constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * kWarp;
+constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * kWarp;  // (warps 10 and 11 only give their registers away)
 constexpr int kPrStages = 5;                         // K and V tiles in the ring
 constexpr uint32_t kHalf = kPrRows * 128;            // 16 KB: 128 rows of 64 channels
 constexpr uint32_t kPrTile = 2 * kHalf;              // 32 KB
@@ -82,10 +81,11 @@ struct PrShared {
     uint64_t answer_full;
     alignas(16) uint32_t answer[4];        // the next item as it is won
     uint64_t item_full[kPrItems], item_empty[kPrItems];
-    alignas(16) PrItem item[kPrItems];     // the items as warp 10 hands them out
+    alignas(16) PrItem item[kPrItems];     // the items as warp 8 hands them out
     uint32_t tmem;
     int32_t abort;
     int32_t not_finite;          // some item's own V was not all finite
+    int32_t cleaned[kPrStages];  // warps that are done with a V tile under the mask
 };
 constexpr size_t kPrSharedBytes = (sizeof(PrShared) + 1023) / 1024 * 1024;  // the tiles start on 1024 bytes
 constexpr size_t kPrSmem = kPrSharedBytes + (size_t)(2 + kPrStages) * kPrTile;
@@ -275,7 +275,7 @@ __device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool repor
 }
 
 // The CTA's items: the grid has one CTA per item, the first has its own index,
-// the next ones those of CTAs that had not started. Warp 10 wins them, looks
+// the next ones those of CTAs that had not started. Warp 8 wins them, looks
 // them up (2000 cycles of dependent loads and divisions) and hands them to the
 // other warps through a ring, ahead of their use.
 struct PrItems {
@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
             mbar_init(smem_u32(&sh.v_raw[i]), 1);
+            sh.cleaned[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.q_full[i]), 1);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         sh.not_finite = 0;
         for (int i = 0; i < kPrItems; ++i) {
             mbar_init(smem_u32(&sh.item_full[i]), 1);
-            mbar_init(smem_u32(&sh.item_empty[i]), kPrSoftmaxWarps + 3);
+            mbar_init(smem_u32(&sh.item_empty[i]), kPrSoftmaxWarps + 1);
         }
         mbar_init(smem_u32(&sh.answer_full), 1);
         mbar_init(smem_u32(&sh.drain), 1);
@@ -343,61 +344,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
     if (warp >= kPrSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsRest));
         if (warp == kPrSoftmaxWarps) {
-            // ---- TMA: an item's first K and V, its Q tiles, the other K and V ----------------
+            // ---- TMA: an item's Q tiles, then K and V of its key tiles --------------------
             int loads = 0;              // K/V tiles asked for so far
             int q_uses[2] = {0, 0};
-            bool ok = true;
-            PrItems items{sh, a.dev_status};
-            for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
-                const PrItem& it = *at;
-                if (lane == 0) {
-                    for (int i = 0; ok && i < 2 * it.n; ++i) {
-                        if (i == 2 || (i == 1 && it.n == 1)) {  // (Q's place is free once the item before is through with it)
-#pragma unroll
-                            for (int w = 0; w < 2; ++w) {
-                                if (!ok || it.first[w] >= it.n) continue;
-                                if (q_uses[w] > 0 && !pr_wait(sh, sh.q_empty[w], (q_uses[w] - 1) & 1, a.dev_status)) ok = false;
-                                ok = ok && !pr_aborted(sh);
-                                if (!ok) continue;
-                                ++q_uses[w];
-                                mbar_arrive_expect_tx(smem_u32(&sh.q_full[w]), (uint32_t)(T * G) * 256u);
-                                for (int h = 0; h < 2; ++h)
-                                    tma_load_4d(sQ + w * kPrTile + h * kHalf, &args.q, 64 * h, 0, it.kvh, it.sq.row0 + it.t[w],
-                                                smem_u32(&sh.q_full[w]));
-                            }
-                            if (!ok) break;
-                        }
-                        const int st = loads % kPrStages;
-                        if (loads >= kPrStages && !pr_wait(sh, sh.empty[st], (loads / kPrStages + 1) & 1, a.dev_status))
-                            ok = false;
-                        if (!ok || pr_aborted(sh)) break;
-                        const int j = it.hi - 1 - (i >> 1);
-                        const int row = (int)(it.sq.off + (int64_t)j * kPrKeys);
-                        const uint32_t bar = (i & 1) && j >= it.masked ? smem_u32(&sh.v_raw[st]) : smem_u32(&sh.full[st]);
-                        mbar_arrive_expect_tx(bar, kPrTile);
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_3d(sKV + st * kPrTile + h * kHalf, (i & 1) ? &args.v : &args.k, 64 * h, it.kvh, row, bar);
-                        ++loads;
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)(ok && !pr_aborted(sh)), 0) != 0;
-                items.done();
-            }
-            if (lane == 0) {  // every issued copy has landed before the CTA can exit
-                for (int i = loads > kPrStages ? loads - kPrStages : 0; i < loads; ++i)
-                    mbar_wait_bounded(smem_u32(&sh.full[i % kPrStages]), (i / kPrStages) & 1, kWaitLimitNs);
-                for (int w = 0; w < 2; ++w)
-                    if (q_uses[w] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[w]), (q_uses[w] - 1) & 1, kWaitLimitNs);
-            }
-        } else if (warp == kPrSoftmaxWarps + 2) {
-            // ---- the items ----------------------------------------------------------------------
             int asked = 0, handed = 0;  // items asked for, handed out
             bool ok = true;
             auto hand_out = [&](const PrItem& it) {
                 const int at = handed % kPrItems;
                 if (handed >= kPrItems)
                     ok = ok && __all_sync(0xffffffffu, pr_wait(sh, sh.item_empty[at], (uint32_t)(handed / kPrItems - 1) & 1u, a.dev_status));
-                ok = ok && !__any_sync(0xffffffffu, pr_aborted(sh));
                 if (!ok) return;
                 if (lane == 0) {
                     sh.item[at] = it;
@@ -413,9 +368,35 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 ++asked;
                 const PrItem it = pr_item(a, i, true);
                 if (it.live) hand_out(it);
-                // (waited for in any case: the answer must have landed before the CTA can exit)
-                const bool got = __all_sync(0xffffffffu, pr_wait(sh, sh.answer_full, (uint32_t)(asked - 1) & 1u, a.dev_status));
-                ok = ok && got;
+                if (lane == 0 && it.live) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || it.first[w] >= it.n) continue;
+                        if (q_uses[w] > 0 && !pr_wait(sh, sh.q_empty[w], (q_uses[w] - 1) & 1, a.dev_status)) ok = false;
+                        ok = ok && !pr_aborted(sh);
+                        if (!ok) continue;
+                        ++q_uses[w];
+                        mbar_arrive_expect_tx(smem_u32(&sh.q_full[w]), (uint32_t)(T * G) * 256u);
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_4d(sQ + w * kPrTile + h * kHalf, &args.q, 64 * h, 0, it.kvh, it.sq.row0 + it.t[w],
+                                        smem_u32(&sh.q_full[w]));
+                    }
+                    for (int i = 0; ok && i < 2 * it.n; ++i) {
+                        const int st = loads % kPrStages;
+                        if (loads >= kPrStages && !pr_wait(sh, sh.empty[st], (loads / kPrStages + 1) & 1, a.dev_status))
+                            ok = false;
+                        if (!ok || pr_aborted(sh)) break;
+                        const int j = it.hi - 1 - (i >> 1);
+                        const int row = (int)(it.sq.off + (int64_t)j * kPrKeys);
+                        const uint32_t bar = (i & 1) && j >= it.masked ? smem_u32(&sh.v_raw[st]) : smem_u32(&sh.full[st]);
+                        mbar_arrive_expect_tx(bar, kPrTile);
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_3d(sKV + st * kPrTile + h * kHalf, (i & 1) ? &args.v : &args.k, 64 * h, it.kvh, row, bar);
+                        ++loads;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)(ok && !pr_aborted(sh)), 0) != 0;
+                ok = ok && __all_sync(0xffffffffu, pr_wait(sh, sh.answer_full, (uint32_t)(asked - 1) & 1u, a.dev_status));
                 if (ok) i = cancelled_cta(smem_u32(sh.answer));
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -423,6 +404,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             PrItem end;
             end.live = -1;
             hand_out(end);
+            if (lane == 0) {  // every issued copy and answer has landed before the CTA can exit
+                if (asked > 0) mbar_wait_bounded(smem_u32(&sh.answer_full), (uint32_t)(asked - 1) & 1u, kWaitLimitNs);
+                for (int i = loads > kPrStages ? loads - kPrStages : 0; i < loads; ++i)
+                    mbar_wait_bounded(smem_u32(&sh.full[i % kPrStages]), (i / kPrStages) & 1, kWaitLimitNs);
+                for (int w = 0; w < 2; ++w)
+                    if (q_uses[w] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[w]), (q_uses[w] - 1) & 1, kWaitLimitNs);
+            }
         } else if (warp == kPrSoftmaxWarps + 1) {
             // ---- MMA issue --------------------------------------------------------------------
             const uint32_t one = elect_one();
@@ -490,46 +478,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 mma_commit(one, smem_u32(&sh.drain));
                 mbar_wait_bounded(smem_u32(&sh.drain), 0, kWaitLimitNs);
             }
-        } else {
-            // ---- V under the mask: elements that are not finite, behind the item's first row's token ----
-            int loads = 0;        // K/V tiles of the items before
-            uint32_t parity = 0;  // of each stage's v_raw
-            bool ok = true;
-            PrItems items{sh, a.dev_status};
-            for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
-                const PrItem& it = *at;
-                for (int s = 0; ok && s < it.n && it.hi - 1 - s >= it.masked; ++s) {
-                    const int j = it.hi - 1 - s, st = (loads + 2 * s + 1) % kPrStages;
-                    ok = __all_sync(0xffffffffu, pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status));
-                    if (!ok) break;
-                    parity ^= 1u << st;
-                    const uint32_t v = sKV + (uint32_t)(st * kPrTile);
-                    const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = it.see - j * kPrKeys;
-                    bool wrote = false;
-#pragma unroll 4
-                    for (int i = 8 * r_lo + lane; i < 16 * kPrKeys - 8 * r_lo; i += kWarp) {
-                        // 16-byte chunks of rows r_lo .. 127 of the first half, then of the second
-                        const int c = i < 8 * kPrKeys ? i : i - 8 * kPrKeys + 8 * r_lo;
-                        const uint32_t to = v + (i < 8 * kPrKeys ? 0u : kHalf) + 16u * (uint32_t)c;
-                        uint4 x = ld_shared_v4(to);
-                        // an exponent of all ones carries into bit 15
-                        auto bad = [](uint32_t e) { return ((e & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                        if (((bad(x.x) | bad(x.y)) | (bad(x.z) | bad(x.w))) == 0u) continue;
-                        uint32_t* e = &x.x;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) e[q] &= ~(((bad(e[q]) >> 15) & 0x00010001u) * 0xffffu);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                                     : "memory");
-                        wrote = true;
-                        if ((c >> 3) < r_end) sh.not_finite = 1;  // (behind it no row of the item sees anything)
-                    }
-                    if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[st]));
-                }
-                loads += 2 * it.n;
-                items.done();
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsSoftmax));
@@ -542,6 +490,52 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         const f32x2 c2 = pair(c, c);
         bool ok = true;
         int u = 0, outs = 0;  // S tiles and outputs so far
+        int loads = 0;        // K/V tiles of the items before
+        uint32_t parity = 0;  // of each stage's v_raw
+        // V of key tile j under the mask, by the four warps of a tile: rows behind
+        // `see` become zeros, elements that are not finite are zeroed and noted.
+        auto clean = [&](const PrItem& it, int j, int st) {
+            if (!pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status)) return;
+            const uint32_t v = sKV + (uint32_t)(st * kPrTile);
+            // keys behind the item's first row: some row does not see them
+            const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = min(kPrKeys, it.see - j * kPrKeys);
+            bool found = false;
+            for (int i = r + 8 * r_lo; i < 8 * kPrKeys; i += 128) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = v + h * kHalf + 16 * i;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    bool put = true;
+                    if ((i >> 3) < r_end) {
+                        x = ld_shared_v4(at);
+                        uint32_t* e = &x.x;
+                        put = false;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const bool lo = (e[q] & 0x7f80u) == 0x7f80u, up = (e[q] & 0x7f800000u) == 0x7f800000u;
+                            put |= lo | up;
+                            e[q] &= (lo ? 0xffff0000u : 0xffffffffu) & (up ? 0x0000ffffu : 0xffffffffu);
+                        }
+                        found |= put;
+                    }
+                    if (put)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                                     : "memory");
+                }
+            }
+            if (found) sh.not_finite = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {  // the last of the four warps passes the tile on
+                __threadfence_block();
+                if (atomicAdd(&sh.cleaned[st], 1) == 3) {
+                    sh.cleaned[st] = 0;
+                    __threadfence_block();
+                    mbar_arrive(smem_u32(&sh.full[st]));
+                }
+            }
+            __syncwarp();
+        };
         PrItems items{sh, a.dev_status};
         for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
             const PrItem& it = *at;
@@ -571,6 +565,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             };
             for (int s = first; s < it.n; s += it.stride, ++u) {
                 const int j = it.hi - 1 - s;
+                if (j >= it.masked && (w == 0 || a.dual || s < it.first[0])) clean(it, j, (loads + 2 * s + 1) % kPrStages);
                 ok = __all_sync(0xffffffffu, pr_wait(sh, sh.s_full[w], u & 1, a.dev_status) && !pr_aborted(sh));
                 if (!ok) break;
                 tmem_fence_after();
@@ -628,6 +623,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
             }
             if (!ok) break;
+            for (int s = 0; s < it.n && it.hi - 1 - s >= it.masked; ++s) parity ^= 1u << (loads + 2 * s + 1) % kPrStages;
+            loads += 2 * it.n;
             // ---- output -------------------------------------------------------------------------
             const bool worked = first < it.n;
             if (worked) {
@@ -667,8 +664,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                         }
                 }
             }
-            // (before the stores: an arrival waits for this thread's stores to be performed)
-            items.done();
             if (mine) {
                 uint32_t x[8];
                 if (a.n_parts == 1) {
@@ -693,6 +688,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             }
             // (the next item's first P V overwrites O once P is passed on, which this warp does after these loads)
             tmem_fence_before();
+            items.done();
         }
     }
     pdl_trigger();
