@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                         found |= put;
                     }
                     if (put)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                                     : "memory");
+                        st_shared_v4(at, x.x, x.y, x.z, x.w);
                 }
             }
             if (found) sh.not_finite = 1;
@@ -700,44 +699,61 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
     }
 }
 
-// One warp per (row, query head): the parts by log-sum-exp.
+// The parts of a (row, query head) by log-sum-exp, `per` warps each (1, 2, 4
+// or 8 of the block's 8).
 constexpr int kPmWarps = 8;
-__global__ void __launch_bounds__(kPmWarps * kWarp) prompt_merge_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kPmWarps * kWarp) prompt_merge_kernel(const __grid_constant__ PromptArgs a, int per) {
     pdl_enter();
-    const int lane = lane_id();
-    const int64_t i = (int64_t)blockIdx.x * kPmWarps + warp_id();  // row * H_q + head
-    if (i >= (int64_t)a.n_rows * a.H_q) return;
-    const int row = (int)(i / a.H_q);
+    __shared__ float s_m[kPmWarps], s_den[kPmWarps];
+    __shared__ float4 s_acc[kPmWarps][kWarp];
+    const int lane = lane_id(), warp = warp_id(), sub = warp % per;
+    const int64_t i = (int64_t)blockIdx.x * (kPmWarps / per) + warp / per;  // row * H_q + head
+    bool live = i < (int64_t)a.n_rows * a.H_q;
+    const int row = live ? (int)(i / a.H_q) : 0;
     // rows of no sequence, or of one that was refused, stay as they were
     const int seq = find_last(a.n_seq, [&](int b) { return a.row_offset[b] <= row; });
     const PrSeq sq = pr_seq(a, seq);
-    if (!sq.ok || row < sq.row0 || row >= sq.row0 + sq.n) return;
+    live = live && sq.ok && row >= sq.row0 && row < sq.row0 + sq.n;
+    const int len = sq.base + sq.n;
+    const int parts = !live ? 0 : a.part_keys > 0 ? (len + a.part_keys - 1) / a.part_keys : a.n_parts;
     const int64_t step = (int64_t)a.n_rows * a.H_q;
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < a.n_parts; s0 += 8) {
+    auto add = [&](float m, float l, float4 v) {
+        if (m == -INFINITY) return;  // a part without keys
+        const float nm = fmaxf(M, m);
+        const float so = exp2f(M - nm), sn = exp2f(m - nm);
+        den = den * so + l * sn;
+        acc.x = acc.x * so + v.x * sn;
+        acc.y = acc.y * so + v.y * sn;
+        acc.z = acc.z * so + v.z * sn;
+        acc.w = acc.w * so + v.w * sn;
+        M = nm;
+    };
+    for (int s0 = 8 * sub; s0 < parts; s0 += 8 * per) {
         float2 ml[8];
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const bool in = s0 + u < a.n_parts;
+            const bool in = s0 + u < parts;
             ml[u] = in ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (s0 + u) * step + i) : make_float2(-INFINITY, 0.f);
             v[u] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + ((s0 + u) * step + i) * kPrD) + lane)
                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (ml[u].x == -INFINITY) continue;  // a part without keys
-            const float nm = fmaxf(M, ml[u].x);
-            const float so = exp2f(M - nm), sn = exp2f(ml[u].x - nm);
-            den = den * so + ml[u].y * sn;
-            acc.x = acc.x * so + v[u].x * sn;
-            acc.y = acc.y * so + v[u].y * sn;
-            acc.z = acc.z * so + v[u].z * sn;
-            acc.w = acc.w * so + v[u].w * sn;
-            M = nm;
-        }
+        for (int u = 0; u < 8; ++u) add(ml[u].x, ml[u].y, v[u]);
     }
+    if (per > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_den[warp] = den;
+        }
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < per; ++w) add(s_m[warp + w], s_den[warp + w], s_acc[warp + w][lane]);
+    }
+    if (!live || sub != 0) return;
     const float inv = 1.f / den;
     reinterpret_cast<uint2*>(a.out + i * kPrD)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -751,6 +767,27 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     p.G = H_q / H_kv;
     p.tile_tokens = kPrRows / p.G;
     const int key_tiles = (max_len + kPrKeys - 1) / kPrKeys;
+    auto workspace = [&]() {
+        if (p.n_parts == 1) return;
+        const size_t rows = (size_t)p.n_parts * n_rows * H_q;
+        p.off_ml = rows * kPrD * 4;
+        p.ws_bytes = (p.off_ml + rows * 8 + 255) / 256 * 256;
+    };
+    // A token or two a sequence (16 (row, query head) columns of a kv head or
+    // fewer): attend_prompt_few.cu, the keys in parts of equal size, twice as
+    // many CTAs as run at once (two an SM) if all sequences had max_len tokens,
+    // 128 parts a row at most. 16 single tokens over up to 3136 tokens, 32/4
+    // heads: here 31 us, there FEW_US us.
+    p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65535;
+    if (p.few) {
+        const int64_t units = (int64_t)n_seq * H_kv;
+        int64_t parts = (4 * (int64_t)num_sms + units - 1) / units;
+        if (parts > 128) parts = 128;
+        p.part_keys = (int)((((int64_t)max_len + parts - 1) / parts + 63) / 64 * 64);
+        p.n_parts = (int)(((int64_t)max_len + p.part_keys - 1) / p.part_keys);
+        workspace();
+        return p;
+    }
     // Few rows a sequence: one row tile holds them, and a CTA's second tile
     // takes every other key tile instead of more rows.
     p.dual = (int64_t)n_rows <= (int64_t)n_seq * p.tile_tokens && key_tiles >= 2 && (int64_t)n_seq * H_kv < num_sms;
@@ -778,30 +815,30 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     }
     p.n_parts = p.dual ? 2 * p.n_splits : p.n_splits;
     p.n_items = slots * H_kv * p.n_splits;
-    p.ws_bytes = 0;
-    if (p.n_parts > 1) {
-        const size_t rows = (size_t)p.n_parts * n_rows * H_q;
-        p.off_ml = rows * kPrD * 4;
-        p.ws_bytes = (p.off_ml + rows * 8 + 255) / 256 * 256;
-    }
+    workspace();
     return p;
 }
 
 cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream) {
-    PrArgs args;
-    args.a = a;
-    if (!tensor_map_rows_bf16(&args.q, a.q, a.n_rows, a.H_kv, a.G, a.q_stride, a.tile_tokens) ||
-        !tensor_map_rows_bf16(&args.k, a.k, a.total_tokens, a.H_kv, 0, a.k_stride, kPrKeys) ||
-        !tensor_map_rows_bf16(&args.v, a.v, a.total_tokens, a.H_kv, 0, a.v_stride, kPrKeys))
-        return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(attend_prompt_kernel, kPrSmem, allowed);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.n_items), dim3(kPrThreads), kPrSmem, stream, 0, args);
+    cudaError_t e;
+    if (p.few) {
+        e = launch_attend_prompt_few(a, p.n_parts, stream);
+    } else {
+        PrArgs args;
+        args.a = a;
+        if (!tensor_map_rows_bf16(&args.q, a.q, a.n_rows, a.H_kv, a.G, a.q_stride, a.tile_tokens) ||
+            !tensor_map_rows_bf16(&args.k, a.k, a.total_tokens, a.H_kv, 0, a.k_stride, kPrKeys) ||
+            !tensor_map_rows_bf16(&args.v, a.v, a.total_tokens, a.H_kv, 0, a.v_stride, kPrKeys))
+            return cudaErrorInvalidValue;
+        static std::atomic<uint64_t> allowed{0};
+        e = allow_smem(attend_prompt_kernel, kPrSmem, allowed);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.n_items), dim3(kPrThreads), kPrSmem, stream, 0, args);
+    }
     if (e != cudaSuccess || p.n_parts == 1) return e;
-    const int64_t warps = (int64_t)a.n_rows * a.H_q;
-    return launch_pdl(prompt_merge_kernel, dim3((unsigned)((warps + kPmWarps - 1) / kPmWarps)), dim3(kPmWarps * kWarp), 0,
-                      stream, 0, a);
+    const int per = p.n_parts <= 8 ? 1 : p.n_parts <= 16 ? 2 : p.n_parts <= 32 ? 4 : 8;  // eight parts in flight a warp
+    const int64_t blocks = ((int64_t)a.n_rows * a.H_q + kPmWarps / per - 1) / (kPmWarps / per);
+    return launch_pdl(prompt_merge_kernel, dim3((unsigned)blocks), dim3(kPmWarps * kWarp), 0, stream, 0, a, per);
 }
 
 }  // namespace lsa

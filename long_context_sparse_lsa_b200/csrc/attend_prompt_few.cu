@@ -1,0 +1,296 @@
+// attend_prompt_few.cu — whole-prompt attention where each sequence has a
+// token or two of new rows: lsa_attend_prompt's form for decoding over a dense
+// cache.
+//
+// With so few rows the work is reading K and V once. A 128-row tile of the
+// tensor-core path (attend_prompt.cu) would be nearly empty and its chain of
+// product, softmax and product (1.7 us a tile) would be the time.
+//
+// Design (B200): grid = (parts of the keys, kv heads, sequences). A warp takes
+// every fourth tile of 16 keys of its CTA's part, through a ring of its own
+// that asynchronous copies fill two tiles ahead (two CTAs' rings: 192 KB per
+// SM). As in attend.cu S^T = K Q^T with
+// the keys as M and the sequence's (row, query head) pairs as N columns, mma
+// m16n8k16 in bf16, online softmax in fp32, O^T += V^T P^T with P^T as bf16
+// through movmatrix. The warps merge through shared memory; the parts of a row
+// are combined by prompt_merge_kernel. A part has a fixed number of keys, so
+// that CTAs are alike whatever the sequences' lengths; those behind a
+// sequence's end have nothing to do.
+#include "common.cuh"
+#include "internal.h"
+
+namespace lsa {
+namespace {
+
+constexpr int kFwWarps = 4, kFwThreads = kFwWarps * kWarp;
+constexpr int kFwTile = 16, kFwRing = 3, kFwD = 128;
+constexpr int kFwRow = kFwD * 2;                       // bytes of a K or V row
+constexpr int kFwTileBytes = 2 * kFwTile * kFwRow;     // K, then V: 8 KB
+constexpr int kFwSmem = kFwWarps * kFwRing * kFwTileBytes;
+constexpr int kFwPark = 36;                            // floats of a lane per column tile: o, m, l
+static_assert(kFwWarps * 4 * kFwPark * kWarp * 4 <= kFwSmem, "the merge area lies in the rings");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte chunk c of row m, so that eight rows' equal chunks fall on all banks.
+__device__ __forceinline__ uint32_t fw_at(int m, int c) { return (uint32_t)(m * kFwRow + 16 * (c ^ (m & 7))); }
+
+// NT: tiles of 8 (row, query head) columns taken at a time.
+template <int NT>
+__global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const __grid_constant__ PromptArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
+    const int g = lane >> 2, t4 = lane & 3;
+    const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+    const int row0 = a.row_offset[seq], n = a.row_offset[seq + 1] - row0;
+    const int len = a.seq_lens[seq];
+    const int64_t off = a.kv_offset[seq];
+    pdl_enter();
+    if (n <= 0) return;
+    if (row0 < 0 || (int64_t)row0 + n > a.n_rows || n > len || len > a.max_len || off < 0 || off + len > a.total_tokens) {
+        if (tid == 0 && part == 0 && kvh == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
+        return;
+    }
+    const int base = len - n;                     // tokens before the first row
+    const int k_lo = part * a.part_keys, k_hi = min(len, k_lo + a.part_keys);
+    if (k_lo >= len) return;
+    const int n_tiles = (k_hi - k_lo + kFwTile - 1) / kFwTile;
+    const int G = a.G, cols = n * G;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFwRing * kFwTileBytes);
+    const uint16_t* kb = a.k + off * a.k_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
+    const uint16_t* vb = a.v + off * a.v_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
+    // a lane copies 16-byte chunk lane % 16 of rows lane / 16, + 2, ...; rows behind the part are zeros
+    auto fetch = [&](int i, int slot) {
+        if (i < n_tiles) {
+            const uint32_t to = ring + (uint32_t)(slot * kFwTileBytes);
+#pragma unroll
+            for (int x = 0; x < kFwTile / 2; ++x) {
+                const int m = 2 * x + (lane >> 4);
+                const int key = k_lo + i * kFwTile + m;
+                const uint32_t nb = key < k_hi ? 16u : 0u;
+                const int64_t at = min(key, k_hi - 1);
+                cp_async16(to + fw_at(m, lane & 15), kb + at * a.k_stride, nb);
+                cp_async16(to + (uint32_t)(kFwTile * kFwRow) + fw_at(m, lane & 15), vb + at * a.v_stride, nb);
+            }
+        }
+        cp_async_commit();
+    };
+
+    for (int c0 = 0; c0 < cols; c0 += 8 * NT) {
+        if (c0 > 0) __syncthreads();  // the merge area of the columns before
+#pragma unroll
+        for (int j = 0; j < kFwRing - 1; ++j) fetch(warp + j * kFwWarps, j);
+        // query fragments, and the keys that the lane's accumulator columns see
+        uint32_t qb[NT][8][2];
+        int sees[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int col = c0 + 8 * t + g;
+            const uint16_t* q = a.q + (int64_t)(row0 + col / G) * a.q_stride + (int64_t)(kvh * G + col % G) * kFwD;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qb[t][ks][x] = col < cols ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * x + 2 * t4)) : 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int own = c0 + 8 * t + 2 * t4 + c;
+                sees[t][c] = own < cols ? base + own / G + 1 : 0;
+            }
+        }
+        float o[NT][8][4], m_run[NT][2], l_run[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) o[t][mt][0] = o[t][mt][1] = o[t][mt][2] = o[t][mt][3] = 0.f;
+            m_run[t][0] = m_run[t][1] = -INFINITY;
+            l_run[t][0] = l_run[t][1] = 0.f;
+        }
+        int slot = 0;
+        for (int i = warp; i < n_tiles; i += kFwWarps) {
+            fetch(i + (kFwRing - 1) * kFwWarps, slot == 0 ? kFwRing - 1 : slot - 1);
+            cp_async_wait<kFwRing - 1>();
+            __syncwarp();
+            const uint32_t kt = ring + (uint32_t)(slot * kFwTileBytes), vt = kt + kFwTile * kFwRow;
+            slot = slot + 1 == kFwRing ? 0 : slot + 1;
+            const int key0 = k_lo + i * kFwTile;
+            const bool masked = key0 + kFwTile > base + 1;  // some column does not see some key of the tile
+            if (masked && n > 1) {
+                // V of the newest tokens: rows before them have weight 0, and 0 times an
+                // element that is not finite is not 0: such elements are zeroed here and
+                // added below, to the rows that see them
+                for (int x = lane; x < kFwTile * 16; x += kWarp) {
+                    const int m = x >> 4;
+                    if (key0 + m <= base || key0 + m >= k_hi) continue;
+                    const uint32_t at = vt + fw_at(m, x & 15);
+                    uint4 y = ld_shared_v4(at);
+                    uint32_t* e = &y.x;
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t bad = ((e[q] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // an exponent of all ones carries
+                        any |= bad;
+                        e[q] &= ~(((bad >> 15) & 0x00010001u) * 0xffffu);
+                    }
+                    if (any) st_shared_v4(at, y.x, y.y, y.z, y.w);
+                }
+                __syncwarp();
+            }
+            // ---- S^T: 16 keys x 8 NT columns ------------------------------------------------
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                uint32_t fr[4];
+                ldmatrix_x4(fr, kt + fw_at((lane & 7) + 8 * (lane >> 3 & 1), 2 * ks + (lane >> 4)));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_bf16(s[t], fr, qb[t][ks][0], qb[t][ks][1]);
+            }
+            // ---- online softmax ---------------------------------------------------------------
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float z[4], mx[2], al[2], mc[2];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    z[c] = s[t][c] * a.scale_log2;
+                    if (masked && key0 + g + 8 * (c >> 1) >= sees[t][c & 1]) z[c] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    mx[c] = fmaxf(z[c], z[c + 2]);
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], k));
+                    mx[c] = fmaxf(m_run[t][c], mx[c]);
+                    mc[c] = mx[c] == -INFINITY ? 0.f : mx[c];
+                    al[c] = ex2(m_run[t][c] - mc[c]);
+                }
+                if (__any_sync(0xffffffffu, mx[0] != m_run[t][0] || mx[1] != m_run[t][1])) {
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[t][mt][c] *= al[c & 1];
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) z[c] = ex2(z[c] - mc[c & 1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m_run[t][c] = mx[c];
+                    l_run[t][c] = l_run[t][c] * al[c] + (z[c] + z[c + 2]);
+                }
+                p[t][0] = movmatrix_trans(pack_bf16(z[0], z[1]));
+                p[t][1] = movmatrix_trans(pack_bf16(z[2], z[3]));
+            }
+            // ---- O^T += V^T P^T -----------------------------------------------------------------
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                uint32_t fr[4];  // channels 16 mt + g, + 8 of keys 2t, 2t+1 and 2t+8, 2t+9
+                ldmatrix_x4_trans(fr, vt + fw_at((lane & 7) + 8 * (lane >> 4), 2 * mt + (lane >> 3 & 1)));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_bf16(o[t][mt], fr, p[t][0], p[t][1]);
+            }
+            if (masked && n > 1) {
+                for (int m = max(0, base + 1 - key0); m < kFwTile && key0 + m < k_hi; ++m) {
+                    const uint16_t* v = a.v + (off + key0 + m) * a.v_stride + (int64_t)kvh * kFwD;
+                    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x = __uint_as_float((uint32_t)v[16 * mt + 8 * h + g] << 16);
+                            if (isfinite(x)) continue;
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int mm = 0; mm < 8; ++mm)
+                                    if (mm == mt) {
+                                        if (key0 + m < sees[t][0]) o[t][mm][2 * h] += x;
+                                        if (key0 + m < sees[t][1]) o[t][mm][2 * h + 1] += x;
+                                    }
+                        }
+                }
+            }
+            __syncwarp();  // the slot may be filled again
+        }
+        cp_async_wait<0>();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) l_run[t][c] += __shfl_xor_sync(0xffffffffu, l_run[t][c], k);
+        __syncthreads();
+        // ---- the warps' results: each combines two of the eight channel tiles -----------------
+        float* park = reinterpret_cast<float*>(smem);  // [warp][NT][kFwPark][32]
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float* x = park + (warp * NT + t) * kFwPark * kWarp + lane;
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[(4 * mt + c) * kWarp] = o[t][mt][c];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                x[(32 + c) * kWarp] = m_run[t][c];
+                x[(34 + c) * kWarp] = l_run[t][c];
+            }
+        }
+        if (c0 + 8 * NT >= cols) pdl_trigger();
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = c0 + 8 * t + 2 * t4 + c;
+                const float* x0 = park + t * kFwPark * kWarp + lane;
+                float M = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kFwWarps; ++w) M = fmaxf(M, x0[(w * NT * kFwPark + 32 + c) * kWarp]);
+                const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int w = 0; w < kFwWarps; ++w) {
+                    const float* x = x0 + w * NT * kFwPark * kWarp;
+                    const float f = ex2(x[(32 + c) * kWarp] - mb);
+                    l += x[(34 + c) * kWarp] * f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) y[q] += x[(4 * (2 * warp + (q >> 1)) + c + 2 * (q & 1)) * kWarp] * f;
+                }
+                if (col >= cols) continue;
+                const int64_t row = (int64_t)(row0 + col / G) * a.H_q + kvh * G + col % G;
+                // channels 16 mt + g and + 8 of mt = 2 warp, 2 warp + 1
+                if (a.n_parts == 1) {
+                    const float inv = 1.f / l;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const __nv_bfloat16 b = __float2bfloat16_rn(y[q] * inv);
+                        a.out[row * kFwD + 16 * (2 * warp + (q >> 1)) + 8 * (q & 1) + g] = *reinterpret_cast<const uint16_t*>(&b);
+                    }
+                    if (a.lse != nullptr && warp == 0 && g == 0) a.lse[row] = (M + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    const int64_t at = (int64_t)part * a.n_rows * a.H_q + row;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) a.part_o[at * kFwD + 16 * (2 * warp + (q >> 1)) + 8 * (q & 1) + g] = y[q];
+                    // (a maximum of -infinity marks an empty part: one of NaN scores alone is not)
+                    if (warp == 0 && g == 0)
+                        reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(l == 0.f ? M : fmaxf(M, -3e38f), l);
+                }
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_prompt_few(const PromptArgs& a, int parts, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed[2];
+    // columns of most sequences: 8 or fewer (one token of up to 8 heads), or more
+    const bool wide = (int64_t)a.n_rows * a.G > (int64_t)a.n_seq * 8;
+    auto kern = wide ? attend_prompt_few_kernel<2> : attend_prompt_few_kernel<1>;
+    const cudaError_t e = allow_smem(kern, kFwSmem, allowed[wide ? 1 : 0]);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)parts, (unsigned)a.H_kv, (unsigned)a.n_seq), dim3(kFwThreads), kFwSmem, stream, 0, a);
+}
+
+}  // namespace lsa

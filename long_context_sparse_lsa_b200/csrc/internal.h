@@ -281,16 +281,20 @@ struct PromptArgs {
     int32_t G, tile_tokens;            // query heads per kv head, tokens per row tile
     int32_t n_splits;                  // key splits of each row tile
     int32_t dual, n_parts;             // a CTA's two tiles are of the same rows; partials per row
+    int32_t part_keys;                 // few rows: keys of a part (else 0)
     float scale_log2;
 };
 struct PromptPlan {
     int G = 1, tile_tokens = 128, n_splits = 1, n_parts = 1;
-    bool dual = false;
+    int part_keys = 0;
+    bool few = false, dual = false;
     int64_t n_items = 0;
     size_t off_ml = 0, ws_bytes = 0;
 };
 PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, int num_sms);
 cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaStream_t stream);
+// A token or two of new rows per sequence (attend_prompt_few.cu).
+cudaError_t launch_attend_prompt_few(const PromptArgs& a, int parts, cudaStream_t stream);
 // bf16 rows of H_kv * group heads of 128 channels, `stride` elements apart, in
 // boxes of 64 channels (128-byte swizzle): group == 0: one head of `tokens`
 // rows (3-D: channel, head, row); else the `group` query heads of one kv head

@@ -235,3 +235,11 @@ def test_same_bits_every_time():
         for _ in range(5):
             c.run()
             assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("H,K", [(8, 1), (16, 1), (32, 4), (4, 4), (6, 2), (64, 1), (40, 2)])
+@pytest.mark.parametrize("rows,lens", [([1] * 5, [1, 2, 17, 640, 3001]), ([2, 1, 0, 1], [2, 900, 40, 64]), ([1, 40, 1, 1], [700, 100, 65, 64]),
+                                       ([1] * 70, [64 + 9 * i for i in range(70)])])
+def test_a_token_or_two(H, K, rows, lens):
+    """Single tokens, a few of them, and among them a sequence of many."""
+    Case(H, K, rows, lens, seed=H, gap=3).run().check()
