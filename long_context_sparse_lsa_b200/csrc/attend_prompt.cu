@@ -774,16 +774,18 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
         p.ws_bytes = (p.off_ml + rows * 8 + 255) / 256 * 256;
     };
     // A token or two a sequence (16 (row, query head) columns of a kv head or
-    // fewer): attend_prompt_few.cu, the keys in parts of equal size, twice as
-    // many CTAs as run at once (two an SM) if all sequences had max_len tokens,
-    // 128 parts a row at most. 16 single tokens over up to 3136 tokens, 32/4
-    // heads: here 31 us, there FEW_US us.
+    // fewer): attend_prompt_few.cu, the keys in parts of equal size: as many
+    // CTAs as run at once (two an SM), but four parts of the longest sequence
+    // at least (so that long and short ones even out), 128 at most, and 128
+    // keys a part. 16 single tokens over up to 3136 tokens, 32/4 heads: 16 us
+    // there, 31 us here; 64 over up to 8000: 93 and 199 us.
     p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65535;
     if (p.few) {
         const int64_t units = (int64_t)n_seq * H_kv;
-        int64_t parts = (4 * (int64_t)num_sms + units - 1) / units;
-        if (parts > 128) parts = 128;
+        int64_t parts = (2 * (int64_t)num_sms + units - 1) / units;
+        parts = parts < 4 ? 4 : parts > 128 ? 128 : parts;
         p.part_keys = (int)((((int64_t)max_len + parts - 1) / parts + 63) / 64 * 64);
+        if (p.part_keys < 128) p.part_keys = 128;
         p.n_parts = (int)(((int64_t)max_len + p.part_keys - 1) / p.part_keys);
         workspace();
         return p;

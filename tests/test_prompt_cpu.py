@@ -35,7 +35,7 @@ def test_refuses_before_launch(kw, want):
 
 def test_workspace_and_launches_follow_the_splits():
     lib = lsa.load_library()
-    for n_seq, n_rows, max_len, split in [(1, 1, 9000, True), (1, 8000, 9000, False), (16, 16, 3136, True), (64, 64, 9000, False),
+    for n_seq, n_rows, max_len, split in [(1, 1, 9000, True), (1, 8000, 9000, False), (16, 16, 3136, True), (64, 64, 9000, True),
                                           (1, 1, 100, False)]:
         p = _prompts(n_seq=n_seq, n_rows=n_rows, max_len=max_len)
         assert lib.lsa_attend_prompt_launches(p, 32, 4, 128) == (2 if split else 1)
