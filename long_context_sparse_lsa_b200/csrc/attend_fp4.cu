@@ -41,16 +41,18 @@
 namespace lsa {
 namespace {
 
-constexpr int kF4Warps = 16;
-constexpr int kF4Threads = kF4Warps * kWarp;
-constexpr int kF4Tile = 16;                                                // entries of an MMA tile
-constexpr int kF4Pair = 2 * kF4Tile;                                       // entries of one step of a warp
-constexpr int kRing = 3;                                                   // steps in a team's ring
+// Warps of a CTA and steps in a team's ring, for NT tiles of 8 query heads:
+// the fragments of 16 query heads need the registers of half as many warps.
+__host__ __device__ constexpr int f4_warps(int nt) { return nt == 1 ? 16 : 8; }
+__host__ __device__ constexpr int f4_ring(int nt) { return nt == 1 ? 3 : 6; }
+constexpr int kF4Pair = 32;                                                // entries of a step: two MMA tiles
 constexpr int kF4HeadStep = kF4Pair * 2 * (kFp4CodeBytes + kFp4Groups);    // 4608: a step of one kv head
-constexpr int kF4RingBytes = kF4Warps * kRing * kF4HeadStep;               // 221,184
+constexpr int kF4RingBytes = f4_warps(1) * f4_ring(1) * kF4HeadStep;       // 221,184, for either NT
 constexpr float kPBits = 10.f;                                             // P is carried as 2^10 p
 constexpr int kF4Park = 36;                                                // floats of a lane: o fragments, m, l
-static_assert(kF4RingBytes <= 227 * 1024 && kF4Warps * 2 * kF4Park * kWarp * 4 <= kF4RingBytes, "shared memory of one CTA");
+static_assert(kF4RingBytes == f4_warps(2) * f4_ring(2) * kF4HeadStep && kF4RingBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(f4_warps(1) * kF4Park * kWarp * 4 <= kF4RingBytes && f4_warps(2) * 2 * kF4Park * kWarp * 4 <= kF4RingBytes,
+              "the merge area reuses the rings");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -85,8 +87,9 @@ __device__ __forceinline__ int v_at(int m, int h, int c) {
 
 // NT: tiles of 8 query heads (H_q / H_kv up to 8 or 16). HPC: kv heads per CTA.
 template <int NT, int HPC>
-__global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_constant__ AttendFp4Args a) {
+__global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(const __grid_constant__ AttendFp4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kWarps = f4_warps(NT), kRing = f4_ring(NT);
     const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
     const int g = lane >> 2, t4 = lane & 3;
     const AttendArgs& b = a.base;
@@ -109,13 +112,13 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
             flag(b.dev_status, seq < 0 || seq >= b.n_seq ? LSA_DEV_BAD_SEQ : LSA_DEV_BAD_LENGTH);
         if (split == 0) {
             float* o = b.out[layer] + ((int64_t)r * b.H_q + hgrp * HPC * ratio) * kFp4D;
-            for (int i = tid; i < HPC * ratio * kFp4D; i += kF4Threads) o[i] = 0.f;
+            for (int i = tid; i < HPC * ratio * kFp4D; i += kWarps * kWarp) o[i] = 0.f;
         }
         return;
     }
 
     // a team of HPC warps, one per kv head, works on every n_sel-th step of 32 entries
-    constexpr int n_sel = kF4Warps / HPC;
+    constexpr int n_sel = kWarps / HPC;
     const int h_local = warp % HPC, wsel = warp / HPC;
     const int kvh = hgrp * HPC + h_local;
     auto team_sync = [&]() {
@@ -441,18 +444,14 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
             const int next = HPC * NT * kF4Park * kWarp;  // to the head's next warp
             float M = -INFINITY;
             for (int j = 0; j < n_sel; ++j) M = fmaxf(M, p0[j * next + (32 + c) * kWarp]);
-            float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+            float l = 0.f, x[2 * n_mt] = {};
             const float base = M == -INFINITY ? 0.f : M;
             for (int j = 0; j < n_sel; ++j) {
                 const float* p = p0 + j * next;
                 const float f = ex2(p[(32 + c) * kWarp] - base);
                 l += p[(34 + c) * kWarp] * f;
-                x[0] += p[(4 * m_lo + c) * kWarp] * f;
-                x[1] += p[(4 * m_lo + c + 2) * kWarp] * f;
-                if (n_mt == 2) {
-                    x[2] += p[(4 * m_lo + 4 + c) * kWarp] * f;
-                    x[3] += p[(4 * m_lo + 6 + c) * kWarp] * f;
-                }
+#pragma unroll
+                for (int k = 0; k < 2 * n_mt; ++k) x[k] += p[(4 * m_lo + 2 * k + c) * kWarp] * f;
             }
             const int hh = 8 * n + 2 * t4 + c;
             if (hh >= ratio) continue;
@@ -462,8 +461,11 @@ __global__ void __launch_bounds__(kF4Threads, 1) attend_fp4_kernel(const __grid_
             // a denominator of 0: no entry (NaN scores give NaN)
             const float to = b.vscale[layer] * (!direct ? 1.f : l == 0.f ? 0.f : 1.f / l);
             dst += kFp4Group * g + 2 * m_lo;
-            if (n_mt == 2) *reinterpret_cast<float4*>(dst) = make_float4(x[0] * to, x[1] * to, x[2] * to, x[3] * to);
-            else *reinterpret_cast<float2*>(dst) = make_float2(x[0] * to, x[1] * to);
+#pragma unroll
+            for (int k = 0; k < 2 * n_mt; k += n_mt == 1 ? 2 : 4) {
+                if (n_mt == 1) *reinterpret_cast<float2*>(dst + k) = make_float2(x[k] * to, x[k + 1] * to);
+                else *reinterpret_cast<float4*>(dst + k) = make_float4(x[k] * to, x[k + 1] * to, x[(k + 2) % (2 * n_mt)] * to, x[(k + 3) % (2 * n_mt)] * to);
+            }
             // (a maximum of -infinity marks an empty partial: one of NaN scores alone is not)
             if (!direct && g == 0 && m_lo == 0)
                 *reinterpret_cast<float2*>(b.part_ml + ((row_q * b.n_splits + split) * b.H_q + qh) * 2) =
@@ -479,7 +481,7 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
     p.head_groups = H_kv / p.hpc;
     const long units = (long)n_q * p.head_groups * G;
     const int steps = (budget + kF4Pair - 1) / kF4Pair;
-    const int n_sel = kF4Warps / p.hpc;
+    const int n_sel = f4_warps(H_q / H_kv > 8 ? 2 : 1) / p.hpc;
     int splits = units > 0 ? (int)(num_sms / units) : 1;  // one CTA per SM, one wave
     // at least two steps a warp: below that the merge of the splits costs more than it saves
     const int max_splits = (steps + 2 * n_sel - 1) / (2 * n_sel);
@@ -502,14 +504,14 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
 cudaError_t launch_attend_fp4(const AttendFp4Args& a, size_t smem_bytes, cudaStream_t stream) {
     const AttendArgs& b = a.base;
     static std::atomic<uint64_t> allowed[6];
-    const int wide = b.H_q / b.H_kv > 8;
+    const bool wide = b.H_q / b.H_kv > 8;
     auto kern = b.hpc == 1 ? (wide ? attend_fp4_kernel<2, 1> : attend_fp4_kernel<1, 1>)
                 : b.hpc == 2 ? (wide ? attend_fp4_kernel<2, 2> : attend_fp4_kernel<1, 2>)
                              : (wide ? attend_fp4_kernel<2, 4> : attend_fp4_kernel<1, 4>);
     cudaError_t e = allow_smem(kern, kF4RingBytes, allowed[wide + 2 * (b.hpc >> 1)]);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(b.n_splits * b.head_groups), (unsigned)b.n_q, (unsigned)b.G);
-    e = launch_pdl(kern, grid, dim3(kF4Threads), smem_bytes, stream, 0, a);
+    e = launch_pdl(kern, grid, dim3((unsigned)(f4_warps(wide ? 2 : 1) * kWarp)), smem_bytes, stream, 0, a);
     if (e != cudaSuccess || b.n_splits == 1) return e;
     return launch_attend_merge(b, stream);
 }

@@ -778,7 +778,7 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     // CTAs as run at once (two an SM), but four parts of the longest sequence
     // at least (so that long and short ones even out), 128 at most, and 128
     // keys a part. 16 single tokens over up to 3136 tokens, 32/4 heads: 16 us
-    // there, 31 us here; 64 over up to 8000: 93 and 199 us.
+    // there, 31 us here; 64 over up to 8000: 89 and 201 us.
     p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65535;
     if (p.few) {
         const int64_t units = (int64_t)n_seq * H_kv;
