@@ -9,7 +9,8 @@ from __future__ import annotations
 
 _BINDING_NAMES = {
     "lsa_hi_block_sums", "lsa_append", "lsa_index", "lsa_attend", "lsa_attend_fp8", "lsa_index_workspace_size",
-    "lsa_attend_workspace_size", "lsa_version", "Batch", "Budget", "LsaError", "library_path",
+    "lsa_attend_workspace_size", "lsa_store_fp4", "lsa_attend_fp4", "lsa_attend_fp4_workspace_size", "lsa_attend_prompt",
+    "lsa_attend_prompt_workspace_size", "lsa_version", "Batch", "Budget", "Prompts", "LsaError", "library_path",
     "load_library",
 }
 

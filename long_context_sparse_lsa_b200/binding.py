@@ -142,6 +142,9 @@ class Prompts:
         return _PROMPTS.pack(n_seq, self.n_rows, self.max_len, 0, self.total_tokens, ro.data_ptr(), ko.data_ptr(),
                              sl.data_ptr())
 
+    def tensors(self) -> tuple:
+        return self.row_offset, self.kv_offset, self.seq_lens
+
     def c(self) -> _Prompts:
         return _Prompts.from_buffer_copy(self.packed())
 
@@ -530,10 +533,20 @@ def lsa_attend_noalloc(q: list, k: list, v: list, index_sets: torch.Tensor, batc
     _check("lsa_attend_noalloc", st)
 
 
-def _here(t: torch.Tensor) -> None:
+def _here(*tensors) -> None:
     """Refuse tensors that are not on the device the call would run on."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+    dev = tensors[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("tensors must be on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _status(t):
+    if t is not None and (t.dtype is not torch.int32 or t.numel() < 1):
+        raise TypeError("dev_status must be an int32 tensor")
+    return _ptr(t)
 
 
 _POINTERS = [struct.Struct(f"@{n}P") for n in range(9)]  # a host array of up to LSA_MAX_LAYERS device pointers
@@ -600,7 +613,6 @@ def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_g
     rows = tuple(k_new[0].shape)
     n_rows, H_kv, d = rows
     T = k[0].shape[0]
-    _here(k_new[0])
     if n_rows != prompts.n_rows or T < prompts.total_tokens:
         raise ValueError("k_new must hold prompts.n_rows rows and the caches prompts.total_tokens")
     kn, k_stride = _rows("k_new", k_new, G, rows)
@@ -612,10 +624,11 @@ def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_g
     if k_round is not None:
         kr = _layers("k_round", k_round, G, torch.bfloat16, rows)
         vr = _layers("v_round", v_round, G, torch.bfloat16, rows)
-    st = lib.lsa_store_fp4(kn, k_stride, vn, v_stride, H_kv, d, prompts.packed(), G, *_scales(k_scale, v_scale, G),
-                           _layers("k", k, G, u8, code), _layers("k_group", k_group, G, u8, group),
-                           _layers("v", v, G, u8, code), _layers("v_group", v_group, G, u8, group), kr, vr,
-                           None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    args = (kn, k_stride, vn, v_stride, H_kv, d, prompts.packed(), G, *_scales(k_scale, v_scale, G),
+            _layers("k", k, G, u8, code), _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
+            _layers("v_group", v_group, G, u8, group), kr, vr, _status(dev_status))
+    _here(*k_new, *v_new, *k, *k_group, *v, *v_group, *(k_round or ()), *(v_round or ()), *prompts.tensors(), dev_status)
+    st = lib.lsa_store_fp4(*args, _stream(stream))
     if st:
         _check("lsa_store_fp4", st)
 
@@ -639,20 +652,19 @@ def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_sc
     rows = tuple(q[0].shape)
     n_q, H_q, d = rows
     T, H_kv, _ = k[0].shape
-    _here(q[0])
     if index_sets.dtype is not torch.int32 or not index_sets.is_contiguous() or index_sets.shape[0] != n_q:
         raise TypeError("index_sets must be a contiguous int32 [n_q, budget] tensor")
     if T < batch.total_tokens or batch.q_seq.numel() != n_q:
         raise ValueError("the caches must hold batch.total_tokens rows, q the batch's rows")
     u8, code, group = torch.uint8, (T, H_kv, d // 2), (T, H_kv, d // 16)
-    st = lib.lsa_attend_fp4(_layers("q", q, G, torch.bfloat16, rows), _layers("k", k, G, u8, code),
-                            _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
-                            _layers("v_group", v_group, G, u8, group), *_scales(k_scale, v_scale, G), H_q, H_kv, d,
-                            index_sets.data_ptr(), index_sets.shape[1], batch.packed(), G,
-                            _layers("out", out, G, torch.float32, rows),
-                            None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.nbytes,
-                            None if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    args = (_layers("q", q, G, torch.bfloat16, rows), _layers("k", k, G, u8, code),
+            _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
+            _layers("v_group", v_group, G, u8, group), *_scales(k_scale, v_scale, G), H_q, H_kv, d,
+            index_sets.data_ptr(), index_sets.shape[1], batch.packed(), G, _layers("out", out, G, torch.float32, rows),
+            _ptr(workspace), 0 if workspace is None else workspace.nbytes, _status(dev_status))
+    _here(*q, *k, *k_group, *v, *v_group, index_sets, batch.kv_offset, batch.seq_lens, batch.q_seq, batch.q_len, *out,
+          workspace, dev_status)
+    st = lib.lsa_attend_fp4(*args, _stream(stream))
     if st:
         _check("lsa_attend_fp4", st)
 
@@ -676,7 +688,6 @@ def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts
     n_rows, H_q, d = q.shape
     T, H_kv = k.shape[:2]
     bf16 = torch.bfloat16
-    _here(q)
     if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or out.dtype is not bf16:
         raise TypeError("q, k, v and out must be bfloat16 tensors")
     if k.shape != (T, H_kv, d) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
@@ -685,10 +696,11 @@ def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts
         raise ValueError("q must hold prompts.n_rows rows, k and v prompts.total_tokens")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n_rows, H_q) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 [n_rows, H_q] tensor")
-    st = lib.lsa_attend_prompt(q.data_ptr(), _row_stride("q", q, H_q, d), k.data_ptr(), _row_stride("k", k, H_kv, d),
-                               v.data_ptr(), _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.packed(), out.data_ptr(),
-                               _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                               _ptr(dev_status), _stream(stream))
+    args = (q.data_ptr(), _row_stride("q", q, H_q, d), k.data_ptr(), _row_stride("k", k, H_kv, d), v.data_ptr(),
+            _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.packed(), out.data_ptr(), _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.nbytes, _status(dev_status))
+    _here(q, k, v, out, *prompts.tensors(), lse, workspace, dev_status)
+    st = lib.lsa_attend_prompt(*args, _stream(stream))
     if st:
         _check("lsa_attend_prompt", st)
 

@@ -133,6 +133,14 @@ def normal_e4m3(shape, seed: int, stream: int, device) -> torch.Tensor:
     return _fill(out, seed, stream, draw)
 
 
+def uniform_u8(shape, lo: int, hi: int, seed: int, stream: int, device) -> torch.Tensor:
+    """Bytes drawn uniformly from lo..hi (4-bit code pairs, E4M3 scales)."""
+    out = torch.empty(shape, dtype=torch.uint8, device=device)
+    span = hi - lo + 1
+    return _fill(out, seed, stream, lambda start, cnt: (
+        _srl(hashes(seed, stream, start, cnt, device), 1) % span + lo).to(torch.uint8))
+
+
 def lognormal_lengths(n: int, median: float, sigma: float, lo: int, hi: int, cap: int,
                       seed: int, stream: int) -> list[int]:
     """Ragged sequence lengths: lognormal(ln median, sigma) drawn with the same
@@ -168,3 +176,6 @@ STREAM_K = 32   # + layer
 STREAM_V = 48   # + layer
 STREAM_K8 = 64  # + layer: FP8 E4M3 K cache
 STREAM_V8 = 80  # + layer: FP8 E4M3 V cache
+STREAM_K4 = 96   # + layer: 4-bit K cache, codes (+ 8: group scales)
+STREAM_V4 = 112  # + layer: 4-bit V cache, codes (+ 8: group scales)
+STREAM_NEW = 128  # + layer: rows a step appends to a 4-bit cache (+ 8: V)

@@ -47,10 +47,14 @@ def _pack(tensors, device):
 
 class LsaStep:
     def __init__(self, wl: Workload, t: Tensors, device="cuda", kv_fp8: bool = False, grouped: bool = False,
-                 si_attend: bool | None = None, fuse_append: bool = True):
+                 si_attend: bool | None = None, fuse_append: bool = True, kv_fp4: bool = False):
         """kv_fp8: the K/V caches are FP8 E4M3 codes (drawn here, per layer,
         with scales k_scale / v_scale) and the attention is lsa_attend_fp8;
         the bf16 caches of `t` are then unused and may be empty.
+        kv_fp4: the K/V caches hold 4-bit codes and E4M3 scales per 16
+        channels (drawn here): the step stores the new tokens' bf16 rows with
+        lsa_store_fp4 and attends with lsa_attend_fp4; the bf16 caches of `t`
+        are unused and may be empty.
         grouped: the decode rows of each sequence (wl.drafts of them) attend
         through lsa_attend_grouped (the rows of a group in one CTA).
         si_attend: attend through lsa_attend_si (sink and window runs as dense
@@ -63,11 +67,16 @@ class LsaStep:
         self.device = device
         self.G = len(t.q)
         self.kv_fp8 = kv_fp8
+        self.kv_fp4 = kv_fp4
         self.grouped = grouped
+        if kv_fp4 and kv_fp8:
+            raise ValueError("the caches hold 4 or 8 bits, not both")
+        if (grouped or si_attend) and kv_fp4:
+            raise ValueError("grouped and dense-run attention read bf16 caches")
         if grouped and (kv_fp8 or wl.prefill_new):
             raise ValueError("grouped attention serves bf16 decode rows")
         if si_attend is None:
-            si_attend = bool(wl.prefill_new) and not kv_fp8 and not grouped and wl.n_seq == 1
+            si_attend = bool(wl.prefill_new) and not kv_fp8 and not kv_fp4 and not grouped and wl.n_seq == 1
         self.si_attend = si_attend
         self.fuse_append = fuse_append
         if kv_fp8:
@@ -76,6 +85,16 @@ class LsaStep:
             self.v8 = [gen.normal_e4m3(shape, wl.seed, gen.STREAM_V8 + g, device) for g in range(self.G)]
             self.k_scale = [0.75 + 0.25 * g for g in range(self.G)]
             self.v_scale = [1.5 - 0.25 * g for g in range(self.G)]
+        if kv_fp4:
+            T, H = wl.total_tokens, wl.H_kv
+            draw = lambda n, lo, hi, stream: [gen.uniform_u8((T, H, n), lo, hi, wl.seed, stream + g, device)
+                                              for g in range(self.G)]
+            # codes over all 16 values, scales 0.125 to 0.9375
+            self.k4, self.v4 = draw(wl.d // 2, 0, 255, gen.STREAM_K4), draw(wl.d // 2, 0, 255, gen.STREAM_V4)
+            self.k4_group = draw(wl.d // 16, 0x20, 0x37, gen.STREAM_K4 + 8)
+            self.v4_group = draw(wl.d // 16, 0x20, 0x37, gen.STREAM_V4 + 8)
+            self.k_scale = [2.0 ** -(g % 3) for g in range(self.G)]
+            self.v_scale = [2.0 ** (g % 2 - 1) for g in range(self.G)]
         self.batch = lsa.Batch(t.kv_offset, t.seq_lens, t.q_seq, t.q_len, max(wl.lens), wl.total_tokens,
                                t.blk_offset if wl.hi_block > 0 else None)
         self.budget = lsa.Budget(wl.sink, wl.window, wl.topk, wl.hi_block, wl.hi_topblocks)
@@ -92,6 +111,8 @@ class LsaStep:
                                                          self.G, wl.drafts)
         elif si_attend:
             ws_a = lsa.lsa_attend_si_workspace_size(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget, self.G)
+        elif kv_fp4:
+            ws_a = lsa.lsa_attend_fp4_workspace_size(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget.length, self.G)
         else:
             ws_a = lsa.lsa_attend_workspace_size(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget.length, self.G)
         self.ws_attend = torch.zeros(max(256, ws_a), dtype=torch.uint8, device=device)
@@ -106,9 +127,16 @@ class LsaStep:
                                dtype=torch.int64, device=device)
             n_seq = len(lens)
             self.k_idx_new = t.k_idx.index_select(0, pos).view(n_seq, self.n_new, wl.d_I).clone()
-            kc, vc = self.kv_caches()
-            self.k_new = [x.index_select(0, pos).view(n_seq, self.n_new, wl.H_kv, wl.d).clone() for x in kc]
-            self.v_new = [x.index_select(0, pos).view(n_seq, self.n_new, wl.H_kv, wl.d).clone() for x in vc]
+            if kv_fp4:
+                rows = (n_seq, self.n_new, wl.H_kv, wl.d)
+                self.k_new = [gen.normal_bf16(rows, wl.seed, gen.STREAM_NEW + g, device) for g in range(self.G)]
+                self.v_new = [gen.normal_bf16(rows, wl.seed, gen.STREAM_NEW + 8 + g, device) for g in range(self.G)]
+                self.newest = lsa.Prompts(torch.arange(n_seq + 1, dtype=torch.int32, device=device) * self.n_new,
+                                          t.kv_offset, t.seq_lens, n_seq * self.n_new, max(lens), wl.total_tokens)
+            else:
+                kc, vc = self.kv_caches()
+                self.k_new = [x.index_select(0, pos).view(n_seq, self.n_new, wl.H_kv, wl.d).clone() for x in kc]
+                self.v_new = [x.index_select(0, pos).view(n_seq, self.n_new, wl.H_kv, wl.d).clone() for x in vc]
 
     # -- the three calls --------------------------------------------------------
     def build_block_sums(self, stream=None):
@@ -146,23 +174,41 @@ class LsaStep:
         self.out_buf, self.out = _pack(self.out, self.device)
 
     def kv_caches(self):
-        """The K and V caches the attention reads (FP8 codes or bf16)."""
-        return (self.k8, self.v8) if self.kv_fp8 else (self.t.k, self.t.v)
+        """The K and V caches that lsa_append fills beside the indexer keys: FP8 codes or bf16 (the 4-bit caches
+        are filled by store())."""
+        return ([], []) if self.kv_fp4 else (self.k8, self.v8) if self.kv_fp8 else (self.t.k, self.t.v)
+
+    def _appended(self):
+        """The new K/V rows that lsa_append copies."""
+        return ([], []) if self.kv_fp4 else (self.k_new, self.v_new)
+
+    def store(self, stream=None):
+        """The newest tokens' K/V rows into the 4-bit caches."""
+        rows = (self.newest.n_rows, self.wl.H_kv, self.wl.d)
+        lsa.lsa_store_fp4([x.view(rows) for x in self.k_new], [x.view(rows) for x in self.v_new], self.k4,
+                          self.k4_group, self.v4, self.v4_group, self.k_scale, self.v_scale, self.newest,
+                          dev_status=self.status, stream=stream)
 
     def append(self, stream=None):
         """The decode append: write the newest tokens' keys and K/V rows and
-        refresh the block sums of their blocks (one launch)."""
+        refresh the block sums of their blocks (one launch; with 4-bit caches
+        one more for the K/V rows)."""
         if self.n_new:
             kc, vc = self.kv_caches()
-            lsa.lsa_append(self.k_idx_new, self.t.k_idx, self.k_new, self.v_new, kc, vc,
+            lsa.lsa_append(self.k_idx_new, self.t.k_idx, *self._appended(), kc, vc,
                            self.wl.hi_block, self.block_sums, self.batch, self.n_new, self.status, stream)
+            if self.kv_fp4:
+                self.store(stream)
 
     def append_index(self, stream=None):
-        """The append and the index call in one: lsa_append_index."""
+        """The append and the index call in one: lsa_append_index (and the
+        K/V rows into 4-bit caches)."""
         kc, vc = self.kv_caches()
-        lsa.lsa_append_index(self.k_idx_new, self.k_new, self.v_new, kc, vc, self.n_new, self.t.q_idx, self.t.k_idx,
+        lsa.lsa_append_index(self.k_idx_new, *self._appended(), kc, vc, self.n_new, self.t.q_idx, self.t.k_idx,
                              self.t.w, self.wl.w_max, self.batch, self.budget, self.sets, self.block_sums,
                              self.ws_index, self.status, stream)
+        if self.kv_fp4:
+            self.store(stream)
 
     def index(self, stream=None):
         lsa.lsa_index(self.t.q_idx, self.t.k_idx, self.t.w, self.wl.w_max, self.batch, self.budget, self.sets,
@@ -172,6 +218,9 @@ class LsaStep:
         if self.kv_fp8:
             lsa.lsa_attend_fp8(self.t.q, self.k8, self.v8, self.k_scale, self.v_scale, self.sets, self.batch,
                                self.out, self.ws_attend, self.status, stream)
+        elif self.kv_fp4:
+            lsa.lsa_attend_fp4(self.t.q, self.k4, self.k4_group, self.v4, self.v4_group, self.k_scale, self.v_scale,
+                               self.sets, self.batch, self.out, self.ws_attend, self.status, stream)
         elif self.grouped:
             lsa.lsa_attend_grouped(self.t.q, self.t.k, self.t.v, self.sets, self.batch, self.wl.drafts, self.out,
                                    self.ws_attend, self.status, stream)
@@ -304,7 +353,7 @@ class LsaStep:
         result crosses to the host as the kernel stores it); otherwise they
         are copied back last."""
         cut = self.in_split
-        direct = not (self.kv_fp8 or self.grouped or self.si_attend) and _device_addressable(h_out)
+        direct = not (self.kv_fp8 or self.kv_fp4 or self.grouped or self.si_attend) and _device_addressable(h_out)
         host_out = []
         if direct:
             for o in self.out:
@@ -360,6 +409,9 @@ class LsaStep:
                                                     wl.drafts)
         elif self.si_attend:
             n_att = lsa.lsa_attend_si_launches(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget, self.G)
+        elif self.kv_fp4:
+            n_att = lsa.lsa_attend_fp4_launches(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget.length, self.G)
+            n_att += 1 if self.n_new else 0  # lsa_store_fp4
         else:
             n_att = lsa.lsa_attend_launches(self.batch, wl.H_q, wl.H_kv, wl.d, self.budget.length, self.G)
         return n_idx + n_att

@@ -12,7 +12,9 @@ import torch
 
 import fp4_plain as fp4
 from long_context_sparse_lsa_b200 import binding as lsa
+from long_context_sparse_lsa_b200 import workloads as wls
 from long_context_sparse_lsa_b200 import build
+from long_context_sparse_lsa_b200.pipeline import LsaStep
 
 P = 0x10000  # a fake, aligned device address: never dereferenced (the call is refused first)
 
@@ -150,7 +152,8 @@ def test_binding_refuses_wrong_tensors():
                     (dict(prompts=lsa.Prompts(pr.row_offset, pr.kv_offset, pr.seq_lens, 4, 10, 10)), ValueError),
                     (dict(prompts=lsa.Prompts(pr.row_offset, pr.kv_offset, pr.seq_lens, 3, 10, 11)), ValueError),
                     (dict(prompts=lsa.Prompts(pr.row_offset.long(), pr.kv_offset, pr.seq_lens, 3, 10, 10)), TypeError),
-                    (dict(prompts=lsa.Prompts(pr.row_offset[:1], pr.kv_offset, pr.seq_lens, 3, 10, 10)), ValueError)]:
+                    (dict(prompts=lsa.Prompts(pr.row_offset[:1], pr.kv_offset, pr.seq_lens, 3, 10, 10)), ValueError),
+                    (dict(dev_status=t(u8, 1)), TypeError), (dict(), ValueError)]:  # (the last: host tensors)
         with pytest.raises(err):
             lsa.lsa_store_fp4(**{**ok, **kw}, stream=0)
     b = lsa.Batch(t(torch.int64, 1), t(torch.int32, 1), t(torch.int32, 3), t(torch.int32, 3), 10, 10)
@@ -160,21 +163,52 @@ def test_binding_refuses_wrong_tensors():
     for kw, err in [(dict(q=[t(f32, 3, 8, 128)]), TypeError), (dict(out=[t(bf, 3, 8, 128)]), TypeError),
                     (dict(index_sets=t(torch.int64, 3, 16)), TypeError), (dict(index_sets=t(torch.int32, 2, 16)), TypeError),
                     (dict(k=[t(u8, 9, 2, 64)]), ValueError), (dict(v=[t(u8, 10, 1, 64)]), TypeError),
-                    (dict(v_scale=[1.0, 1.0]), ValueError), (dict(q=[t(bf, 2, 8, 128)]), TypeError)]:
+                    (dict(v_scale=[1.0, 1.0]), ValueError), (dict(q=[t(bf, 2, 8, 128)]), TypeError),
+                    (dict(dev_status=t(u8, 1)), TypeError), (dict(), ValueError)]:
         with pytest.raises(err):
             lsa.lsa_attend_fp4(**{**ok, **kw}, stream=0)
+
+
+def _step(wl, **kw):
+    return LsaStep(wl, wls.make(wl, "cpu", with_kv=False), "cpu", kv_fp4=True, **kw)
+
+
+def test_decode_step_over_a_4_bit_cache():
+    """The step's buffers, launches and refusals, without a GPU."""
+    small = wls.small(wls.BATCH128K, lens=(300, 70), drafts=2, G=2, seed=7)
+    st = _step(small)
+    assert st.k4[1].shape == (370, 4, 64) and st.v4_group[0].shape == (370, 4, 8)
+    assert all(fp4.E4M3[0x20] == 0.125 <= fp4.E4M3[x.numpy()].min() and fp4.E4M3[x.numpy()].max() <= 0.9375
+               for x in st.k4_group + st.v4_group)
+    assert st.newest.row_offset.tolist() == [0, 2, 4] and st.k_new[1].shape == (2, 2, 4, 128)
+    before = [x.clone() for x in [*st.k_new, *st.v_new]]
+    st.pack_io()
+    assert all(torch.equal(x, y) for x, y in zip(before, [*st.k_new, *st.v_new]))
+    for wl in (wls.BATCH128K, wls.CTX1M):  # the store is a launch of its own
+        cut = wls.small(wl, lens=tuple(min(n, 4096) for n in wl.lens))
+        st, t = _step(cut), wls.make(cut, "cpu")
+        st16 = LsaStep(cut, t, "cpu")
+        for x in (st, st16):
+            x.batch.max_len = max(wl.lens)
+        assert st.kernels_per_step() == st16.kernels_per_step() + 1
+    for kw in (dict(kv_fp8=True), dict(grouped=True), dict(si_attend=True)):
+        with pytest.raises(ValueError):
+            _step(small, **kw)
+    chunk = _step(wls.small(wls.PREFILL, lens=(300,), prefill_new=20))
+    assert chunk.n_new == 0 and not chunk.si_attend
 
 
 @pytest.mark.skipif(shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"),
                     reason="nvcc not available")
 def test_no_register_spills():
-    """The 4-bit kernels spill nothing, but for the attention over groups of 16 query heads."""
+    """The kernels keep their fragments in registers; the 4-bit attention spills up to 36 bytes of addresses, outside
+    its loop over the entries."""
     nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
-    for src in ("store_fp4.cu", "attend_fp4.cu"):
+    for src, allowed in (("store_fp4.cu", 0), ("attend_fp4.cu", 36), ("attend_prompt.cu", 0), ("attend_prompt_few.cu", 0)):
         r = subprocess.run([nvcc, *build.ARCH, *build.NVCC_FLAGS, "-Xptxas", "-v", "-c", os.path.join(build.CSRC, src), "-o",
                             os.path.join(build.BUILD_DIR, "ptxas_check_fp4.o")], capture_output=True, text=True)
         assert r.returncode == 0, r.stderr[-2000:]
         found = re.findall(r"Function properties for (\S+)\s+\d+ bytes stack frame, (\d+) bytes spill stores", r.stderr)
         assert found
         for fn, spill in found:
-            assert int(spill) <= (400 if "attend_fp4_kernelILi2E" in fn else 0), (fn, spill)
+            assert int(spill) <= allowed, (fn, spill)

@@ -54,6 +54,7 @@ def test_binding_refuses_wrong_tensors():
                     (dict(k=t(bf, 9, 2, 128), v=t(bf, 9, 2, 128)), ValueError), (dict(out=t(bf, 3, 4, 128)), ValueError),
                     (dict(out=t(bf, 3, 16, 128)[:, ::2]), ValueError), (dict(q=t(bf, 3, 16, 128)[:, ::2]), ValueError),
                     (dict(q=t(bf, 2, 8, 128), out=t(bf, 2, 8, 128)), ValueError),
-                    (dict(lse=t(bf, 3, 8)), TypeError), (dict(lse=t(torch.float32, 8, 3).T), TypeError)]:
+                    (dict(lse=t(bf, 3, 8)), TypeError), (dict(lse=t(torch.float32, 8, 3).T), TypeError),
+                    (dict(dev_status=t(bf, 1)), TypeError), (dict(), ValueError)]:  # (the last: host tensors)
         with pytest.raises(err):
             lsa.lsa_attend_prompt(**{**ok, **kw}, stream=0)
