@@ -44,9 +44,10 @@ PROFILES = os.path.join(ROOT, "profiles")
 # ---------------------------------------------------------------------------
 # algorithmic bytes (what the method must move; nothing avoided by HI counted)
 # ---------------------------------------------------------------------------
-def step_bytes(wl, kv_fp8: bool = False) -> dict:
+def step_bytes(wl, kv_fp8: bool = False, kv_fp4: bool = False) -> dict:
     n_q, G = wl.n_q, wl.G
-    kv_row = wl.H_kv * wl.d * (1 if kv_fp8 else 2)  # bytes of one token's K (or V) in one layer
+    # bytes of one token's K (or V) in one layer; in 4 bits, the codes and a scale per 16 channels
+    kv_row = wl.H_kv * (wl.d // 2 + wl.d // 16 if kv_fp4 else wl.d if kv_fp8 else wl.d * 2)
     rows = _rows(wl)
     attend = 0
     for L in rows:
@@ -67,11 +68,13 @@ def step_bytes(wl, kv_fp8: bool = False) -> dict:
     if wl.prefill_new:  # one cache shared by every row of the chunk: read it once
         index = wl.lens[0] * wl.d_I + n_q * (wl.H_I * wl.d_I + wl.H_I * 4 + wl.budget * 4)
     # decode append per sequence: the new tokens' key and K/V rows read and
-    # written once; with HI on, one block of keys re-read and its sum written
+    # written once (read as bf16 where the cache holds 4 bits); with HI on, one
+    # block of keys re-read and its sum written
+    new_row = wl.H_kv * wl.d * 2 if kv_fp4 else kv_row
     app = 0
     if not wl.prefill_new:
         for L in wl.lens:
-            app += 2 * wl.drafts * (wl.d_I + 2 * G * kv_row)
+            app += 2 * wl.drafts * (wl.d_I + G * (new_row + kv_row))
             if wl.hi_block > 0:
                 app += wl.hi_block * wl.d_I + 2 * wl.d_I
     return {"attend": attend, "index": index, "append": app, "total": attend + index + app}
@@ -458,14 +461,14 @@ def job_rate(units_per_rank: int, world: int, ms: float) -> float:
 
 # ---------------------------------------------------------------------------
 def time_workload(wl, dev, flush, stream, steps, warmup, pg=None, clocks=None, kv_fp8=False, grouped=False,
-                  fuse_append=True):
+                  fuse_append=True, kv_fp4=False):
     """Draws the workload, captures its step graphs and times `steps` steps
     (after `warmup`), each after an L2 flush: the whole step graph for the
     headline, then the three calls one by one for the breakdown."""
     from long_context_sparse_lsa_b200.pipeline import LsaStep
 
-    t = wls.make(wl, dev, with_kv=not kv_fp8)
-    st = LsaStep(wl, t, dev, kv_fp8=kv_fp8, grouped=grouped, fuse_append=fuse_append)
+    t = wls.make(wl, dev, with_kv=not (kv_fp8 or kv_fp4))
+    st = LsaStep(wl, t, dev, kv_fp8=kv_fp8, kv_fp4=kv_fp4, grouped=grouped, fuse_append=fuse_append)
     st.pack_io()  # one input and one output buffer per step (the e2e leg copies each once)
     st.build_block_sums()
     torch.cuda.synchronize()
@@ -585,13 +588,13 @@ def secondary(dev, flush, stream, steps, warmup, peak, fuse_append=True):
         int8 = measure_int8_peak(dev)
     except Exception as exc:  # reported, never silently replaced by an assumed figure
         int8 = {"tops": None, "kind": f"int8 GEMM unavailable: {exc!r}"}
-    for wl, fp8 in ((wls.CTX1M, False), (wls.PREFILL, False), (wls.BATCH128K, True), (wls.ragged(), False),
-                    (wls.DRAFTS128K, False)):
-        drafts = wl.drafts > 1
-        run = time_workload(wl, dev, flush, stream, steps, warmup, kv_fp8=fp8, fuse_append=fuse_append)
+    for wl, kv in ((wls.CTX1M, ""), (wls.PREFILL, ""), (wls.BATCH128K, "fp8"), (wls.BATCH128K, "fp4"),
+                   (wls.ragged(), ""), (wls.DRAFTS128K, "")):
+        drafts, fp8, fp4 = wl.drafts > 1, kv == "fp8", kv == "fp4"
+        run = time_workload(wl, dev, flush, stream, steps, warmup, kv_fp8=fp8, kv_fp4=fp4, fuse_append=fuse_append)
         st = run["st"]
         ms = run["ms"]
-        byts = step_bytes(wl, kv_fp8=fp8)
+        byts = step_bytes(wl, kv_fp8=fp8, kv_fp4=fp4)
         if drafts:
             # concurrent draft rows of a sequence read each K/V row they share
             # from HBM once (L2 holds it for the others): count the union
@@ -643,6 +646,12 @@ def secondary(dev, flush, stream, steps, warmup, peak, fuse_append=True):
                         "value": wl.n_q / (ms / 1000.0), "kv_cache": "fp8 e4m3, one scale per layer for K and V",
                         "note": "same workload as the headline with the K/V caches held as FP8 codes "
                                 "(lsa_attend_fp8); attention bytes per query halve"})
+        elif fp4:
+            rec.update({"metric": "LSA decode queries/s at 128K ctx, 4-bit KV cache", "unit": "queries/s",
+                        "value": wl.n_q / (ms / 1000.0),
+                        "kv_cache": "e2m1 codes, an e4m3 scale per 16 channels, one scale per layer for K and V",
+                        "note": "same workload as the headline with the K/V caches held in 4 bits (the new rows "
+                                "quantised by lsa_store_fp4, attention by lsa_attend_fp4)"})
         elif drafts:
             # the same step with the draft rows of a sequence attended together
             # (lsa_attend_grouped), for comparison
@@ -669,7 +678,7 @@ def secondary(dev, flush, stream, steps, warmup, peak, fuse_append=True):
             rec.update({"metric": "LSA decode queries/s, ragged batch", "unit": "queries/s",
                         "value": wl.n_q / (ms / 1000.0), "layers_per_index": wl.G, "n_seq": wl.n_seq,
                         "cached_tokens": wl.total_tokens, "min_len": min(wl.lens), "max_len": max(wl.lens)})
-        out[wl.name + ("_fp8kv" if fp8 else "")] = rec
+        out[wl.name + (f"_{kv}kv" if kv else "")] = rec
         del run, st
         torch.cuda.synchronize()
         torch.cuda.empty_cache()

@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import bench
 import fp4_plain as fp4
 from long_context_sparse_lsa_b200 import binding as lsa
 from long_context_sparse_lsa_b200 import workloads as wls
@@ -167,6 +168,15 @@ def test_binding_refuses_wrong_tensors():
                     (dict(dev_status=t(u8, 1)), TypeError), (dict(), ValueError)]:
         with pytest.raises(err):
             lsa.lsa_attend_fp4(**{**ok, **kw}, stream=0)
+
+
+def test_step_bytes_with_a_4_bit_cache():
+    b16, b4 = bench.step_bytes(wls.BATCH128K), bench.step_bytes(wls.BATCH128K, kv_fp4=True)
+    # per row and layer 3136 entries, K and V of 4 kv heads: 256 B there, 64 of codes and 8 of scales here
+    assert b16["attend"] - b4["attend"] == 16 * 2 * 3136 * 4 * (256 - 72)
+    # per sequence: the new token's K and V read as bf16 in both, written in 4 bits
+    assert b16["append"] - b4["append"] == 16 * 2 * 4 * (256 - 72)
+    assert b4["index"] == b16["index"]
 
 
 def _step(wl, **kw):
