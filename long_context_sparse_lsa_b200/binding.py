@@ -1,6 +1,7 @@
 """Python binding of liblsa.so (include/lsa.h): argument marshalling only.
 
-Every function takes torch tensors, passes their device pointers and sizes to
+Every function takes torch tensors, passes their device pointers and sizes (the
+longest argument lists through _marshal, csrc/marshal.cpp) to
 the C ABI on the current CUDA stream, and raises LsaError on a non-zero
 status. Every step of the hot path runs in the library's CUDA kernels; there
 is no fallback. If the library is missing, loading it raises immediately.
@@ -8,14 +9,15 @@ is no fallback. If the library is missing, loading it raises immediately.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
-import struct
 from dataclasses import dataclass
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblsa.so")
+_MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 
 LSA_DEV_BAD_LENGTH = 0x1
 LSA_DEV_BAD_SEQ = 0x2
@@ -68,11 +70,6 @@ class _Prompts(ctypes.Structure):
                 ("row_offset", ctypes.c_void_p), ("kv_offset", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
 
 
-# the same two structures for struct.pack (native alignment)
-_BATCH, _PROMPTS = struct.Struct("@4iq5P"), struct.Struct("@4iq3P")
-assert _BATCH.size == ctypes.sizeof(_Batch) and _PROMPTS.size == ctypes.sizeof(_Prompts)
-
-
 @dataclass
 class Budget:
     sink: int
@@ -100,22 +97,17 @@ class Batch:
     total_tokens: int
     blk_offset: torch.Tensor | None = None  # int64 [n_seq]
 
-    def packed(self) -> bytes:
-        """lsa_batch_t as bytes (cheaper to build and to pass than a ctypes structure)."""
-        ko, sl, qs, ql, bo = self.kv_offset, self.seq_lens, self.q_seq, self.q_len, self.blk_offset
-        i32, i64 = torch.int32, torch.int64
-        if not (ko.dtype is i64 and sl.dtype is i32 and qs.dtype is i32 and ql.dtype is i32 and ko.is_contiguous()
-                and sl.is_contiguous() and qs.is_contiguous() and ql.is_contiguous()):
-            for name, t, dt in (("kv_offset", ko, i64), ("seq_lens", sl, i32), ("q_seq", qs, i32), ("q_len", ql, i32)):
-                if t.dtype != dt or not t.is_contiguous():
-                    raise TypeError(f"{name} must be a contiguous {dt} tensor")
-        if bo is not None and (bo.dtype is not i64 or not bo.is_contiguous()):
-            raise TypeError("blk_offset must be a contiguous int64 tensor")
-        return _BATCH.pack(sl.numel(), qs.numel(), int(self.max_len), 0, int(self.total_tokens), ko.data_ptr(),
-                           sl.data_ptr(), 0 if bo is None else bo.data_ptr(), qs.data_ptr(), ql.data_ptr())
-
     def c(self) -> _Batch:
-        return _Batch.from_buffer_copy(self.packed())
+        for name, t, dt in (("kv_offset", self.kv_offset, torch.int64), ("seq_lens", self.seq_lens, torch.int32),
+                            ("q_seq", self.q_seq, torch.int32), ("q_len", self.q_len, torch.int32)):
+            if t.dtype != dt or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dt} tensor")
+        if self.blk_offset is not None and (self.blk_offset.dtype != torch.int64 or not self.blk_offset.is_contiguous()):
+            raise TypeError("blk_offset must be a contiguous int64 tensor")
+        return _Batch(int(self.seq_lens.numel()), int(self.q_seq.numel()), int(self.max_len), 0,
+                      int(self.total_tokens), self.kv_offset.data_ptr(), self.seq_lens.data_ptr(),
+                      self.blk_offset.data_ptr() if self.blk_offset is not None else None,
+                      self.q_seq.data_ptr(), self.q_len.data_ptr())
 
 
 @dataclass
@@ -130,23 +122,16 @@ class Prompts:
     max_len: int
     total_tokens: int
 
-    def packed(self) -> bytes:
-        """lsa_prompts_t as bytes."""
-        ro, ko, sl = self.row_offset, self.kv_offset, self.seq_lens
-        if (ro.dtype is not torch.int32 or ko.dtype is not torch.int64 or sl.dtype is not torch.int32
-                or not (ro.is_contiguous() and ko.is_contiguous() and sl.is_contiguous())):
-            raise TypeError("row_offset and seq_lens must be contiguous int32, kv_offset contiguous int64 tensors")
-        n_seq = sl.numel()
-        if ro.numel() != n_seq + 1 or ko.numel() != n_seq:
-            raise ValueError("row_offset must hold n_seq + 1 values, kv_offset and seq_lens n_seq")
-        return _PROMPTS.pack(n_seq, self.n_rows, self.max_len, 0, self.total_tokens, ro.data_ptr(), ko.data_ptr(),
-                             sl.data_ptr())
-
-    def tensors(self) -> tuple:
-        return self.row_offset, self.kv_offset, self.seq_lens
-
     def c(self) -> _Prompts:
-        return _Prompts.from_buffer_copy(self.packed())
+        for name, t, dt in (("row_offset", self.row_offset, torch.int32), ("kv_offset", self.kv_offset, torch.int64),
+                            ("seq_lens", self.seq_lens, torch.int32)):
+            if t.dtype != dt or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dt} tensor")
+        n_seq = int(self.seq_lens.numel())
+        if self.row_offset.numel() != n_seq + 1 or self.kv_offset.numel() != n_seq:
+            raise ValueError("row_offset must hold n_seq + 1 values, kv_offset and seq_lens n_seq")
+        return _Prompts(n_seq, int(self.n_rows), int(self.max_len), 0, int(self.total_tokens),
+                        self.row_offset.data_ptr(), self.kv_offset.data_ptr(), self.seq_lens.data_ptr())
 
 
 _lib = None
@@ -161,8 +146,9 @@ def load_library():
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m long_context_sparse_lsa_b200.build`")
+    for path in (LIB_PATH, _MARSHAL_PATH):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m long_context_sparse_lsa_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     lib.lsa_version.restype = i32
@@ -246,6 +232,10 @@ def load_library():
     lib.lsa_attend_noalloc.restype = i32
     lib.lsa_attend_noalloc.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i32, i32, vp,
                                        i32, ctypes.POINTER(_Batch), i32, ctypes.POINTER(vp), vp, vp]
+    # the calls whose arguments _marshal (csrc/marshal.cpp) checks and hands over
+    lib.marshal = importlib.import_module("._marshal", __package__)
+    for name in ("store_fp4", "attend_fp4", "attend_prompt"):
+        setattr(lib, name + "_at", ctypes.cast(getattr(lib, "lsa_" + name), vp).value)
     _lib = lib
     return lib
 
@@ -256,8 +246,8 @@ def _check(func: str, status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the 3 us of the stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -533,74 +523,6 @@ def lsa_attend_noalloc(q: list, k: list, v: list, index_sets: torch.Tensor, batc
     _check("lsa_attend_noalloc", st)
 
 
-def _here(*tensors) -> None:
-    """Refuse tensors that are not on the device the call would run on."""
-    dev = tensors[0].get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device")
-
-
-def _status(t):
-    if t is not None and (t.dtype is not torch.int32 or t.numel() < 1):
-        raise TypeError("dev_status must be an int32 tensor")
-    return _ptr(t)
-
-
-_POINTERS = [struct.Struct(f"@{n}P") for n in range(9)]  # a host array of up to LSA_MAX_LAYERS device pointers
-_FLOATS = [struct.Struct(f"@{n}f") for n in range(9)]
-
-
-def _layers(name: str, ts: list, n: int, dtype: torch.dtype, shape: tuple) -> bytes:
-    """The device pointers of a per-layer list of contiguous tensors, as a host array."""
-    if len(ts) != n:
-        raise ValueError(f"{name} must hold one tensor per layer")
-    ptrs = []
-    for t in ts:
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            raise TypeError(f"{name} must hold contiguous {dtype} tensors of shape {shape}")
-        ptrs.append(t.data_ptr())
-    return _POINTERS[n].pack(*ptrs)
-
-
-def _layer_count(ts: list) -> int:
-    if not 1 <= len(ts) <= 8:
-        raise ValueError("1 to 8 layers")
-    return len(ts)
-
-
-def _scales(k_scale: list, v_scale: list, n: int) -> tuple[bytes, bytes]:
-    if len(k_scale) != n or len(v_scale) != n:
-        raise ValueError("k_scale and v_scale must hold one scale per layer")
-    return _FLOATS[n].pack(*k_scale), _FLOATS[n].pack(*v_scale)
-
-
-def _rows(name: str, ts: list, n: int, shape: tuple) -> tuple[bytes, int]:
-    """Device pointers and row stride of a per-layer list of bf16 [rows, H, d] views, all with the same stride."""
-    if len(ts) != n:
-        raise ValueError(f"{name} must hold one tensor per layer")
-    ptrs, stride = [], None
-    for t in ts:
-        if t.dtype is not torch.bfloat16 or t.shape != shape:
-            raise TypeError(f"{name} must hold bfloat16 tensors of shape {shape}")
-        s = _row_stride(name, t, shape[1], shape[2])
-        if stride is not None and s != stride:
-            raise ValueError(f"{name}: every layer must have the same row stride")
-        stride = s
-        ptrs.append(t.data_ptr())
-    return _POINTERS[n].pack(*ptrs), stride
-
-
-def _row_stride(name: str, t: torch.Tensor, H: int, d: int) -> int:
-    """Elements from one token to the next of a [tokens, H, d] view whose heads are contiguous."""
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if t.shape[0] > 1 else H * d
-
-
 def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_group: list, k_scale: list, v_scale: list,
                   prompts: Prompts, k_round: list | None = None, v_round: list | None = None,
                   dev_status: torch.Tensor | None = None, stream=None) -> None:
@@ -608,27 +530,10 @@ def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_g
     projection, are taken as they are) into 4-bit caches (codes uint8 [T, H_kv, 64], group scales uint8 E4M3
     [T, H_kv, 8]) with per-layer power-of-two scales. k_round, v_round: the values the caches now hold (bf16
     [n_rows, H_kv, 128])."""
-    lib = load_library()
-    G = _layer_count(k_new)
-    rows = tuple(k_new[0].shape)
-    n_rows, H_kv, d = rows
-    T = k[0].shape[0]
-    if n_rows != prompts.n_rows or T < prompts.total_tokens:
-        raise ValueError("k_new must hold prompts.n_rows rows and the caches prompts.total_tokens")
-    kn, k_stride = _rows("k_new", k_new, G, rows)
-    vn, v_stride = _rows("v_new", v_new, G, rows)
-    u8, code, group = torch.uint8, (T, H_kv, d // 2), (T, H_kv, d // 16)
-    if (k_round is None) != (v_round is None):
-        raise ValueError("k_round and v_round come together")
-    kr = vr = None
-    if k_round is not None:
-        kr = _layers("k_round", k_round, G, torch.bfloat16, rows)
-        vr = _layers("v_round", v_round, G, torch.bfloat16, rows)
-    args = (kn, k_stride, vn, v_stride, H_kv, d, prompts.packed(), G, *_scales(k_scale, v_scale, G),
-            _layers("k", k, G, u8, code), _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
-            _layers("v_group", v_group, G, u8, group), kr, vr, _status(dev_status))
-    _here(*k_new, *v_new, *k, *k_group, *v, *v_group, *(k_round or ()), *(v_round or ()), *prompts.tensors(), dev_status)
-    st = lib.lsa_store_fp4(*args, _stream(stream))
+    lib, p = load_library(), prompts
+    st = lib.marshal.store_fp4(lib.store_fp4_at, k_new, v_new, k, k_group, v, v_group, k_scale, v_scale, p.row_offset,
+                               p.kv_offset, p.seq_lens, p.n_rows, p.max_len, p.total_tokens, k_round, v_round, dev_status,
+                               stream)
     if st:
         _check("lsa_store_fp4", st)
 
@@ -647,24 +552,9 @@ def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_sc
                    dev_status: torch.Tensor | None = None, stream=None) -> None:
     """lsa_attend over 4-bit K/V caches: codes uint8 [T, H_kv, 64], group scales uint8 E4M3 [T, H_kv, 8], per-layer
     scales (lists of G tensors and floats)."""
-    lib = load_library()
-    G = _layer_count(q)
-    rows = tuple(q[0].shape)
-    n_q, H_q, d = rows
-    T, H_kv, _ = k[0].shape
-    if index_sets.dtype is not torch.int32 or not index_sets.is_contiguous() or index_sets.shape[0] != n_q:
-        raise TypeError("index_sets must be a contiguous int32 [n_q, budget] tensor")
-    if T < batch.total_tokens or batch.q_seq.numel() != n_q:
-        raise ValueError("the caches must hold batch.total_tokens rows, q the batch's rows")
-    u8, code, group = torch.uint8, (T, H_kv, d // 2), (T, H_kv, d // 16)
-    args = (_layers("q", q, G, torch.bfloat16, rows), _layers("k", k, G, u8, code),
-            _layers("k_group", k_group, G, u8, group), _layers("v", v, G, u8, code),
-            _layers("v_group", v_group, G, u8, group), *_scales(k_scale, v_scale, G), H_q, H_kv, d,
-            index_sets.data_ptr(), index_sets.shape[1], batch.packed(), G, _layers("out", out, G, torch.float32, rows),
-            _ptr(workspace), 0 if workspace is None else workspace.nbytes, _status(dev_status))
-    _here(*q, *k, *k_group, *v, *v_group, index_sets, batch.kv_offset, batch.seq_lens, batch.q_seq, batch.q_len, *out,
-          workspace, dev_status)
-    st = lib.lsa_attend_fp4(*args, _stream(stream))
+    lib, b = load_library(), batch
+    st = lib.marshal.attend_fp4(lib.attend_fp4_at, q, k, k_group, v, v_group, k_scale, v_scale, index_sets, b.kv_offset,
+                                b.seq_lens, b.q_seq, b.q_len, b.max_len, b.total_tokens, out, workspace, dev_status, stream)
     if st:
         _check("lsa_attend_fp4", st)
 
@@ -684,23 +574,9 @@ def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts
     """Causal attention of the prompts' rows over every token each sees: q bf16 [n_rows, H_q, 128], k and v bf16
     [T, H_kv, 128] (views whose rows are apart, as of a fused projection, are taken as they are), out bf16 [n_rows,
     H_q, 128], lse fp32 [n_rows, H_q] or None."""
-    lib = load_library()
-    n_rows, H_q, d = q.shape
-    T, H_kv = k.shape[:2]
-    bf16 = torch.bfloat16
-    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or out.dtype is not bf16:
-        raise TypeError("q, k, v and out must be bfloat16 tensors")
-    if k.shape != (T, H_kv, d) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("k and v must be [T, H_kv, d], out contiguous [n_rows, H_q, d]")
-    if n_rows != prompts.n_rows or T < prompts.total_tokens:
-        raise ValueError("q must hold prompts.n_rows rows, k and v prompts.total_tokens")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n_rows, H_q) or not lse.is_contiguous()):
-        raise TypeError("lse must be a contiguous float32 [n_rows, H_q] tensor")
-    args = (q.data_ptr(), _row_stride("q", q, H_q, d), k.data_ptr(), _row_stride("k", k, H_kv, d), v.data_ptr(),
-            _row_stride("v", v, H_kv, d), H_q, H_kv, d, prompts.packed(), out.data_ptr(), _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.nbytes, _status(dev_status))
-    _here(q, k, v, out, *prompts.tensors(), lse, workspace, dev_status)
-    st = lib.lsa_attend_prompt(*args, _stream(stream))
+    lib, p = load_library(), prompts
+    st = lib.marshal.attend_prompt(lib.attend_prompt_at, q, k, v, p.row_offset, p.kv_offset, p.seq_lens, p.n_rows, p.max_len,
+                                   p.total_tokens, out, workspace, lse, dev_status, stream)
     if st:
         _check("lsa_attend_prompt", st)
 

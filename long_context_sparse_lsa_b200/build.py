@@ -1,7 +1,8 @@
-"""Build liblsa.so (the C-ABI library) from csrc/*.cu for sm_100a.
+"""Build liblsa.so (the C-ABI library) from csrc/*.cu for sm_100a, and
+_marshal.so (compiled argument handling of binding.py) from csrc/marshal.cpp.
 
 Usage: python -m long_context_sparse_lsa_b200.build [--force] [--verbose]
-The library is written next to this file (in-tree) so it travels with the
+Both are written next to this file (in-tree) so they travel with the
 source tree; nvcc cross-compiles without a GPU.
 """
 from __future__ import annotations
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liblsa.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -40,16 +43,36 @@ def _deps() -> list[str]:
     out = []
     for d in (CSRC, INCLUDE):
         for f in os.listdir(d):
-            if f.endswith((".cu", ".cuh", ".h")):
+            if f.endswith((".cu", ".cuh", ".h", ".cpp")):
                 out.append(os.path.join(d, f))
     return out
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not (os.path.exists(LIBRARY) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIBRARY)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _deps() + [os.path.abspath(__file__)])
+
+
+def _build_marshal(nvcc: str, verbose: bool) -> None:
+    """_marshal.so, against the headers and libraries of the installed torch (which the importing process has loaded)."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *["-I" + d for d in inc], os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(base, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -72,7 +95,9 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        marshal = ex.submit(_build_marshal, nvcc, verbose)
         objs = list(ex.map(compile_one, sources()))
+        marshal.result()
     tmp = LIBRARY + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     if verbose:
