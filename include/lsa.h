@@ -52,8 +52,8 @@
  *  - Kernels are launched with programmatic stream serialisation: a kernel
  *    may start before the preceding kernel on the stream has finished when
  *    that kernel allows it (griddepcontrol.launch_dependents), and it reads
- *    the batch's row metadata (q_seq, q_len, kv_offset, seq_lens, blk_offset)
- *    before waiting for it; everything else is read after the wait. A caller
+ *    the batch's row metadata (q_seq, q_len, kv_offset, seq_lens, blk_offset,
+ *    row_offset) before waiting for it; everything else is read after the wait. A caller
  *    whose own kernels trigger dependent launches must write those arrays
  *    before triggering.
  */

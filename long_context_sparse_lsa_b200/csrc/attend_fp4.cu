@@ -482,13 +482,24 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
     const long units = (long)n_q * p.head_groups * G;
     const int steps = (budget + kF4Pair - 1) / kF4Pair;
     const int n_sel = f4_warps(H_q / H_kv > 8 ? 2 : 1) / p.hpc;
-    int splits = units > 0 ? (int)(num_sms / units) : 1;  // one CTA per SM, one wave
-    // at least two steps a warp: below that the merge of the splits costs more than it saves
-    const int max_splits = (steps + 2 * n_sel - 1) / (2 * n_sel);
-    if (splits > max_splits) splits = max_splits;
-    if (splits < 1) splits = 1;
-    int per = (steps + splits - 1) / splits;
-    if (per < 1) per = 1;
+    // Splits: the shortest of (waves of CTAs, one an SM) x (rounds of a CTA's
+    // teams, and its start and end) + the merge, in us: a round takes 2.5 (2 with
+    // 16 query heads), a CTA's start and end 6, a merge 3 and a little per split.
+    // At 3136 entries, 32/4 heads, measured for each count of splits (1, 3, the
+    // chosen one): 4 rows 65, 29, 12 us (37 splits); 16 rows 65, 29, 17 (9);
+    // 80 rows 67, 60, 60; 128 rows 69, 87, 69 (1); 163 rows 133, 112, 112.
+    const double round = H_q / H_kv > 8 ? 2.0 : 2.5;
+    int per = steps > 0 ? steps : 1;
+    double best = 0;
+    for (int s = 1; s <= 64 && s <= steps; ++s) {
+        const int each = (steps + s - 1) / s, parts = (steps + each - 1) / each;
+        const long waves = (units * parts + num_sms - 1) / num_sms;
+        const double t = (double)waves * (round * ((each + n_sel - 1) / n_sel) + 6) + (parts > 1 ? 3 + 0.03 * parts : 0);
+        if (s == 1 || t < 0.97 * best) {
+            best = t;
+            per = each;
+        }
+    }
     p.entries_per_split = per * kF4Pair;
     p.n_splits = steps > 0 ? (steps + per - 1) / per : 1;
     p.smem_bytes = kF4RingBytes;
