@@ -45,7 +45,7 @@ constexpr int kPrD = 128;
 constexpr int kPrRows = 128;                         // rows of a tile
 constexpr int kPrKeys = 128;                         // keys of a tile
 constexpr int kPrSoftmaxWarps = 8;                    // four per row tile
-constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * kWarp;  // (warps 10 and 11 only give their registers away)
+constexpr int kPrThreads = (kPrSoftmaxWarps + 4) * kWarp;
 constexpr int kPrStages = 5;                         // K and V tiles in the ring
 constexpr uint32_t kHalf = kPrRows * 128;            // 16 KB: 128 rows of 64 channels
 constexpr uint32_t kPrTile = 2 * kHalf;              // 32 KB
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         sh.not_finite = 0;
         for (int i = 0; i < kPrItems; ++i) {
             mbar_init(smem_u32(&sh.item_full[i]), 1);
-            mbar_init(smem_u32(&sh.item_empty[i]), kPrSoftmaxWarps + 1);
+            mbar_init(smem_u32(&sh.item_empty[i]), kPrSoftmaxWarps + 3);
         }
         mbar_init(smem_u32(&sh.answer_full), 1);
         mbar_init(smem_u32(&sh.drain), 1);
@@ -478,6 +478,62 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 mma_commit(one, smem_u32(&sh.drain));
                 mbar_wait_bounded(smem_u32(&sh.drain), 0, kWaitLimitNs);
             }
+        } else {
+            // ---- V under the mask: rows behind `see` become zeros, elements that are
+            // not finite in rows that some row of the item does not see are zeroed and noted
+            const int half = warp - kPrSoftmaxWarps - 2;  // two warps, every other 16 bytes x 32 each
+            int loads = 0;
+            uint32_t parity = 0;  // of each stage's v_raw
+            bool ok = true;
+            PrItems items{sh, a.dev_status};
+            for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
+                const int n = at->n, hi = at->hi, masked = at->masked, see = at->see, first_key = at->sq.base + at->t[0] + 1;
+                for (int s = 0; ok && s < n && hi - 1 - s >= masked; ++s) {
+                    const int j = hi - 1 - s, st = (loads + 2 * s + 1) % kPrStages;
+                    ok = __all_sync(0xffffffffu, pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status) && !pr_aborted(sh));
+                    if (!ok) break;
+                    parity ^= 1u << st;
+                    const uint32_t v = sKV + (uint32_t)(st * kPrTile);
+                    const int r_lo = max(0, first_key - j * kPrKeys), r_end = min(kPrKeys, see - j * kPrKeys);
+                    uint32_t found = 0;
+                    // 16 bytes of 8 rows' worth at a time: a row of 64 channels is 8 pieces
+                    for (int i = 8 * r_lo + 32 * half + lane; i < 8 * r_end; i += 64) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t p = v + h * kHalf + 16 * i;
+                            uint4 x = ld_shared_v4(p);
+                            uint32_t* e = &x.x;
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t bad = ((e[q] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // an exponent of all ones carries
+                                any |= bad;
+                                e[q] &= ~(((bad >> 15) & 0x00010001u) * 0xffffu);
+                            }
+                            found |= any;
+                            if (any) st_shared_v4(p, x.x, x.y, x.z, x.w);
+                        }
+                    }
+                    for (int i = 8 * max(r_lo, r_end) + 32 * half + lane; i < 8 * kPrKeys; i += 64) {
+                        st_shared_v4(v + 16 * i, 0, 0, 0, 0);
+                        st_shared_v4(v + kHalf + 16 * i, 0, 0, 0, 0);
+                    }
+                    if (found) sh.not_finite = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {  // the second of the two warps passes the tile on
+                        __threadfence_block();
+                        if (atomicAdd(&sh.cleaned[st], 1) == 1) {
+                            sh.cleaned[st] = 0;
+                            __threadfence_block();
+                            mbar_arrive(smem_u32(&sh.full[st]));
+                        }
+                    }
+                    __syncwarp();
+                }
+                loads += 2 * n;
+                items.done();
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsSoftmax));
@@ -490,51 +546,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         const f32x2 c2 = pair(c, c);
         bool ok = true;
         int u = 0, outs = 0;  // S tiles and outputs so far
-        int loads = 0;        // K/V tiles of the items before
-        uint32_t parity = 0;  // of each stage's v_raw
-        // V of key tile j under the mask, by the four warps of a tile: rows behind
-        // `see` become zeros, elements that are not finite are zeroed and noted.
-        auto clean = [&](const PrItem& it, int j, int st) {
-            if (!pr_wait(sh, sh.v_raw[st], parity >> st & 1u, a.dev_status)) return;
-            const uint32_t v = sKV + (uint32_t)(st * kPrTile);
-            // keys behind the item's first row: some row does not see them
-            const int r_lo = max(0, it.sq.base + it.t[0] + 1 - j * kPrKeys), r_end = min(kPrKeys, it.see - j * kPrKeys);
-            bool found = false;
-            for (int i = r + 8 * r_lo; i < 8 * kPrKeys; i += 128) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = v + h * kHalf + 16 * i;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    bool put = true;
-                    if ((i >> 3) < r_end) {
-                        x = ld_shared_v4(at);
-                        uint32_t* e = &x.x;
-                        put = false;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const bool lo = (e[q] & 0x7f80u) == 0x7f80u, up = (e[q] & 0x7f800000u) == 0x7f800000u;
-                            put |= lo | up;
-                            e[q] &= (lo ? 0xffff0000u : 0xffffffffu) & (up ? 0x0000ffffu : 0xffffffffu);
-                        }
-                        found |= put;
-                    }
-                    if (put)
-                        st_shared_v4(at, x.x, x.y, x.z, x.w);
-                }
-            }
-            if (found) sh.not_finite = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {  // the last of the four warps passes the tile on
-                __threadfence_block();
-                if (atomicAdd(&sh.cleaned[st], 1) == 3) {
-                    sh.cleaned[st] = 0;
-                    __threadfence_block();
-                    mbar_arrive(smem_u32(&sh.full[st]));
-                }
-            }
-            __syncwarp();
-        };
         PrItems items{sh, a.dev_status};
         for (const PrItem* at = items.next(); ok && at != nullptr; at = items.next()) {
             const PrItem& it = *at;
@@ -564,7 +575,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             };
             for (int s = first; s < it.n; s += it.stride, ++u) {
                 const int j = it.hi - 1 - s;
-                if (j >= it.masked && (w == 0 || a.dual || s < it.first[0])) clean(it, j, (loads + 2 * s + 1) % kPrStages);
                 ok = __all_sync(0xffffffffu, pr_wait(sh, sh.s_full[w], u & 1, a.dev_status) && !pr_aborted(sh));
                 if (!ok) break;
                 tmem_fence_after();
@@ -622,8 +632,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[w]));
             }
             if (!ok) break;
-            for (int s = 0; s < it.n && it.hi - 1 - s >= it.masked; ++s) parity ^= 1u << (loads + 2 * s + 1) % kPrStages;
-            loads += 2 * it.n;
             // ---- output -------------------------------------------------------------------------
             const bool worked = first < it.n;
             if (worked) {
