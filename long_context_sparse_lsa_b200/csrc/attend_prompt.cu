@@ -4,7 +4,8 @@
 // one of attend.cu.
 //
 // Design (B200): S = Q K^T and O += P V on tcgen05.mma (bf16, fp32
-// accumulators in tensor memory), persistent CTAs over work items (row tiles of a kv head and, for few rows, a split of the keys).
+// accumulators in tensor memory), persistent CTAs over work items (row tiles of
+// a kv head and, for few rows, a split of the keys).
 //  * Rows: one tile of 128 rows is T = 128 / G tokens x the G query heads of
 //    one kv head, so that all of them share K and V, a short prompt fills its
 //    tiles and the causal border wastes at most one 128-key tile per T tokens.
@@ -18,9 +19,11 @@
 //    threads per row, with half the keys each and the maximum exchanged
 //    through shared memory, were no faster: 1959 against 1929 us for a prompt
 //    of 16384 tokens, 32/4 heads.)
-//  * Warp 8 loads Q and a ring of 128-key K and V tiles by TMA; warp 9 issues
-//    the MMAs. Every role walks the same items, so an item's loads and first
-//    products run under the end of the item before.
+//  * Warp 8 wins the items (the grid has a CTA for each; one that runs takes
+//    over those that have not started), looks them up, loads Q and a ring of
+//    128-key K and V tiles by TMA; warp 9 issues the MMAs. Every role walks the
+//    same items, so an item's loads and first products run under the end of the
+//    item before.
 //  * The output is rescaled only when a row's maximum has risen by more than
 //    2^8 over the one in use, with the next tile, or by more than 2^16, at once
 //    (P stays below 2^16, sums are fp32): the softmax threads do it themselves,
@@ -31,8 +34,15 @@
 //    V rows behind every row of the CTA (other sequences' rows, rows never
 //    written) are zeroed in shared memory, and elements that are not finite
 //    within the CTA's own tokens are zeroed and added back at the end, by each
-//    row that sees them (the softmax warps do this while they wait for S).
+//    row that sees them. Warps 10 and 11 clean the tiles beside the first softmax
+//    (by the softmax warps, before it: 157 us for 24 ragged prompts, 150 so).
 //  * Partials of split keys are combined by prompt_merge_kernel by log-sum-exp.
+//  * What bounds it: the chain of one row tile, softmax (1950 cycles), P V (512),
+//    the next S (512) and their hand-overs (350), whose tensor part the other row
+//    tile's fills to 61%; with long prompts the board's power as well (1.6 to
+//    1.7 GHz): 16384 tokens, 32/4 heads, 1130 TFLOP/s. Short prompts (24 of up to
+//    1500 tokens: 650 TFLOP/s) add 8000 cycles an item for the first S, the
+//    masked tile and the output.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
 #include "internal.h"
