@@ -131,32 +131,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
-// Pairs of floats in one register pair: one instruction for both.
-using f32x2 = uint64_t;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(f32x2 x, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2_down(f32x2 x, f32x2 y) {  // rounds towards -infinity
-    f32x2 r;
-    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-
 // P of 32 scores as bf16 pairs, and their sum onto sum[0..1]: 2^(z c - mc),
 // kPoly of the 16 pairs on the FMA units, beside the special-function unit, whose 16 results a clock and SM are half of what the tensor
 // core's tiles ask for (128 columns of one warp a scheduler: 1519 cycles

@@ -9,19 +9,23 @@
 // s == 0 stores codes 0; a group with a number that is not finite stores the
 // scale NaN (0x7f) and codes 0, and sets LSA_DEV_BAD_VALUE.
 //
-// Exact rounding in fp32. x / S is exact (a power of two). x has at most 8
-// significant bits and s at most 4, so a border t between two codes (a
-// multiple of 1/4, 3 bits) and x / (s S) are either equal or at least
-// t * 2^-8 >= 2^-10 apart: the quotient taken by a reciprocal (off by a few
-// 2^-24) and then rounded to a multiple of 2^-13 is on the right side of
-// every border and exactly on it in a tie. The same holds for max|x| / (6 S)
-// and E4M3's borders (5 significant bits), where one IEEE division per group
-// does.
+// Exact rounding in fp32. A power of two changes no significant bit, so S = 1
+// below. x has at most 8 significant bits and s at most 4. A border t between
+// two codes is a multiple of 1/4 of 3 bits: t and x / s are equal or at least
+// t * 2^-8 >= 2^-10 apart. The quotient by a reciprocal (off by a few 2^-24)
+// rounded to a multiple of 2^-13 is therefore on the right side of every border,
+// and exactly on it in a tie. For the scale, a border b of E4M3 has 5 bits and
+// 6 b has 7: it and max|x| are equal or more than 2^-8 of themselves apart, so
+// max|x| * (1/6) rounded to 12 significant bits is on b's right side, and on b
+// in a tie.
 //
 // Bound: HBM bytes (2 read, 9/16 written per number, 2 more with the rounded
-// rows); with a few rows, the latency of the dependent loads. One thread per
-// group: 32 bytes in, 8 code bytes and 1 scale byte out, consecutive threads
-// on consecutive groups, so that every access of a warp is a run.
+// rows: 306 MB for 65536 tokens of 4 heads, 52 us); with a few rows, the latency
+// of the dependent loads. With an IEEE division and reciprocal per group, a
+// 64-bit division per thread and seven operations per number the instructions
+// bound it (85% of the issue slots, 56 us). One thread per group: 32 bytes in, 8
+// code bytes and 1 scale byte out, consecutive threads on consecutive groups,
+// so that every access of a warp is a run.
 #include "fp4.cuh"
 #include "internal.h"
 
@@ -54,25 +58,29 @@ __device__ __forceinline__ void quantise(const Groups16& in, float S, float inv_
     for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
     top = max(top & 0xffffu, top >> 16);
     out.bad = top >= 0x7f80u;
-    const float want = __fdiv_rn(__uint_as_float(top << 16) * inv_S, 6.f);
+    const float sixth = fminf(__uint_as_float(top << 16) * (inv_S * (1.f / 6.f)), 1024.f);
+    const float up = __fmul_rn(sixth, 4097.f);  // to 12 significant bits (not to be fused into one operation)
+    const float want = __fsub_rn(up, __fsub_rn(up, sixth));
     const uint32_t byte = (uint32_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
     out.scale = out.bad ? kE4m3NaN : byte;
     const float s = e4m3_to_f32(out.scale);
     const bool live = !out.bad && byte != 0;
-    const float f = live ? __frcp_rn(s) : 0.f;
+    float f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
+    f = live ? f * inv_S : 0.f;
+    // 1536 = 1.5 * 2^10: adding it rounds to a multiple of 2^-13 (numbers it does not
+    // fit are above 6 on either side of the rounding)
+    const f32x2 f2 = pair(f, f), big = pair(1536.f, 1536.f), neg_big = pair(-1536.f, -1536.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float r[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t x = w[4 * h + i];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float v = e ? bf16_hi(x) : bf16_lo(x);
-                // 1536 = 1.5 * 2^10: adding it rounds to a multiple of 2^-13
-                const float t = (fminf(fabsf(v) * inv_S * f, 8.f) + 1536.f) - 1536.f;
-                r[2 * i + e] = copysignf(t, v);
-            }
+            const float lo = bf16_lo(w[4 * h + i]), hi = bf16_hi(w[4 * h + i]);
+            float t0, t1;
+            unpair(add2(fma2(pair(lo, hi), f2, big), neg_big), t0, t1);
+            r[2 * i] = copysignf(t0, lo);
+            r[2 * i + 1] = copysignf(t1, hi);
         }
         out.code[h] = live ? f32_to_e2m1x8(r) : 0u;
     }
@@ -85,7 +93,9 @@ __device__ __forceinline__ void quantise(const Groups16& in, float S, float inv_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-                out.value[4 * h + i] = pack_bf16(v.x * sS, v.y * sS);
+                float v0, v1;
+                unpair(mul2(pair(v.x, v.y), pair(sS, sS)), v0, v1);
+                out.value[4 * h + i] = pack_bf16(v0, v1);
             }
         }
     }
@@ -98,11 +108,12 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
     const int tid = threadIdx.x;
     const int layer = blockIdx.y >> 1, is_v = blockIdx.y & 1;
     const int per_row = a.H_kv * kFp4Groups;
-    const int64_t g0 = (int64_t)blockIdx.x * kStThreads;
-    const int64_t idx = g0 + tid;
-    const int row0 = (int)(g0 / per_row);
-    const int row = (int)(idx / per_row);
-    const int in_row = (int)(idx - (int64_t)row * per_row);
+    // the CTA's 32 (row, head) pairs (their number fits 32 bits, as n_rows * H_kv does)
+    const uint32_t pair0 = blockIdx.x * (uint32_t)(kStThreads / kFp4Groups), H = (uint32_t)a.H_kv;
+    const uint32_t first = pair0 / H, head = pair0 - first * H + (uint32_t)(tid / kFp4Groups);
+    const int row0 = (int)first;
+    const int row = row0 + (int)(head / H);
+    const int in_row = (int)(head % H) * kFp4Groups + tid % kFp4Groups;
     const bool live = row < a.n_rows;
     pdl_enter();
     Groups16 x = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -114,7 +125,7 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
     }
     // cache rows of the CTA's tokens
     if (tid < kWarp) {
-        const int last = min(a.n_rows - 1, (int)((g0 + kStThreads - 1) / per_row));
+        const int last = min(a.n_rows - 1, (int)((pair0 + kStThreads / kFp4Groups - 1) / H));
         int seq = find_last(a.n_seq, [&](int b) { return a.row_offset[b] <= row0; });
         for (int i = tid; i <= last - row0; i += kWarp) {
             const int r = row0 + i;
