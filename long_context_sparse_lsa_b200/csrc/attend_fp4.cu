@@ -10,10 +10,13 @@
 //    4 kv heads over one run of set entries; a team of one warp per kv head
 //    works on every n-th step of 32 entries.
 //  * A team gathers its steps itself with 16-byte asynchronous copies into a
-//    ring of three, whole tokens at a time (the heads' codes of a token are
-//    256 consecutive bytes, their scales 32): 64 rows of 3136 random tokens
-//    take 46 us this way from HBM, 90 us when each warp fetches its own
-//    head's 64 + 8 bytes, and 60 us as one bulk copy per token.
+//    ring, whole tokens at a time (the heads' codes of a token are 256
+//    consecutive bytes, their scales 32): 64 rows of 3136 random tokens take
+//    46 us this way from HBM, 90 us when each warp fetches its own head's
+//    64 + 8 bytes, and 60 us as one bulk copy per token.
+//  * 16 warps, or 8 for 9 to 16 query heads per kv head: their fragments need
+//    255 registers a thread (16 warps of 128, spilling 500 bytes: 64 rows of
+//    64/4 heads, two layers 134 us; 8 warps 104).
 //  * S^T = K Q^T on fp16 tensor cores (mma.m16n8k16): 16 tokens are M, the
 //    group's query heads N. Lane (g, t) holds the 32 channels 32 t .. 32 t +
 //    31 of tokens g and g + 8 (one 16-byte read per token) and the query
@@ -29,12 +32,17 @@
 //    scale group) of tokens 2t, 2t+1, 2t+8, 2t+9; the codes of a token pair
 //    are interleaved so that the conversion yields the (token, token + 1)
 //    pairs of the A fragment, and the pair's scales multiply them. Each
-//    tile's product is summed on its own and added to the rescaled running
+//    step's product is summed on its own and added to the rescaled running
 //    output in fp32 arithmetic: the tensor core truncates its sums, and 400
 //    truncations into one accumulator cost 2e-6 of the output at 64 rows of
 //    3136 entries.
 //  * The warps of a kv head merge through shared memory by log-sum-exp; one
 //    partial per split, combined by attend_merge_kernel.
+//  * What bounds it: where every SM has a CTA with many steps, the instructions
+//    (a step of a head is about 650; 61% of the issue slots, the integer pipe
+//    with the conversions 51%): 64 rows of 3136 entries, two layers: 68 us, 235
+//    MB at 3.4 TB/s, on 128 of 148 SMs. With few rows the chain of row lookup,
+//    set, gather, products and merge: 12 us for one row of four layers.
 #include "fp4.cuh"
 #include "internal.h"
 
