@@ -115,6 +115,24 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
     const bool bad = seq < 0 || seq >= b.n_seq || L < 1 || L > b.max_len || L > slen || off < 0 ||
                      off + slen > b.total_tokens;
     pdl_enter();
+
+    // a team of HPC warps, one per kv head, works on every n_sel-th step of 32 entries;
+    // a lane holds one entry of a step (-1: none). The first entries are asked for
+    // before the row's lookup above is waited for.
+    constexpr int n_sel = kWarps / HPC;
+    const int h_local = warp % HPC, wsel = warp / HPC;
+    const int e0 = split * b.entries_per_split;
+    const int n_local = max(0, min(b.budget - e0, b.entries_per_split));
+    const int n_steps = (n_local + kF4Pair - 1) / kF4Pair;
+    const int32_t* set = b.sets + (int64_t)r * b.budget + e0;
+    // (loaded here, checked where it is used: the check waits for the load)
+    auto entry = [&](int i) -> int {
+        const int at = i * kF4Pair + lane;
+        return i < n_steps && at < n_local ? __ldg(set + at) : -1;
+    };
+    int ent[kRing];  // entries of the steps in flight; the last is not asked for (and not checked) yet
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) ent[j] = entry(wsel + j * n_sel);
     if (bad) {
         if (tid == 0 && blockIdx.x == 0 && layer == 0)
             flag(b.dev_status, seq < 0 || seq >= b.n_seq ? LSA_DEV_BAD_SEQ : LSA_DEV_BAD_LENGTH);
@@ -125,9 +143,6 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
         return;
     }
 
-    // a team of HPC warps, one per kv head, works on every n_sel-th step of 32 entries
-    constexpr int n_sel = kWarps / HPC;
-    const int h_local = warp % HPC, wsel = warp / HPC;
     const int kvh = hgrp * HPC + h_local;
     auto team_sync = [&]() {
         if (HPC == 1) __syncwarp();
@@ -135,16 +150,6 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
     };
 
     // ---- gather: a team's steps, kRing - 1 in flight, each warp 32 / HPC whole tokens --
-    // A lane holds one entry of a step (-1: none).
-    const int e0 = split * b.entries_per_split;
-    const int n_local = max(0, min(b.budget - e0, b.entries_per_split));
-    const int n_steps = (n_local + kF4Pair - 1) / kF4Pair;
-    const int32_t* set = b.sets + (int64_t)r * b.budget + e0;
-    // (loaded here, checked where it is used: the check waits for the load)
-    auto entry = [&](int i) -> int {
-        const int at = i * kF4Pair + lane;
-        return i < n_steps && at < n_local ? __ldg(set + at) : -1;
-    };
     auto checked = [&](int e) -> int {
         if (e >= -1 && e < L) return e;
         flag(b.dev_status, LSA_DEV_BAD_INDEX);
@@ -212,9 +217,6 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
         }
         cp_async_commit();
     };
-    int ent[kRing];  // entries of the steps in flight; the last is not asked for (and not checked) yet
-#pragma unroll
-    for (int j = 0; j < kRing; ++j) ent[j] = entry(wsel + j * n_sel);
 #pragma unroll
     for (int j = 0; j < kRing - 1; ++j) {
         ent[j] = checked(ent[j]);
