@@ -346,3 +346,57 @@ def test_same_bits_every_time():
     for _ in range(5):
         c.run()
         assert all(torch.equal(x, y) for x, y in zip(first, c.out))
+
+
+def test_store_changed_lengths_in_a_captured_call():
+    """A graph whose row offsets and lengths change between replays; rows behind the last sequence are not stored."""
+    lens, rows, H = [300, 500], [40, 24], 2
+    pr = _prompts(rows, lens, 900, max_len=600)
+    new = [_rand((64, H, 128), i) for i in (1, 2)]
+    caches = _caches(900, H, 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    store = lambda: lsa.lsa_store_fp4(new[:1], new[1:], *caches, [0.5], [2.0], pr, dev_status=status)
+    store()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        store()
+    for n_rows, n_lens in (([40, 24], [300, 500]), ([0, 64], [7, 64]), ([1, 1], [1, 600]), ([0, 0], [0, 0])):
+        pr.row_offset.copy_(_i32([0, n_rows[0], sum(n_rows)]))
+        pr.seq_lens.copy_(_i32(n_lens))
+        pr.kv_offset.copy_(_i64([3, 300]))
+        for x in caches:
+            x[0].fill_(0xA5)
+        for i in (0, 1):
+            new[i].copy_(_rand((64, H, 128), sum(n_lens) + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        at = np.concatenate([np.arange(o + n - r, o + n) for o, n, r in zip((3, 300), n_lens, n_rows)]).astype(int)
+        for i, (code, group, sc) in enumerate(((caches[0], caches[1], 0.5), (caches[2], caches[3], 2.0))):
+            wc, wg, _ = fp4.quantise(new[i], sc)
+            full_c, full_g = np.full((900, H, 64), 0xA5, np.uint8), np.full((900, H, 8), 0xA5, np.uint8)
+            full_c[at], full_g[at] = wc[:len(at)], wg[:len(at)]
+            assert np.array_equal(code[0].cpu().numpy(), full_c) and np.array_equal(group[0].cpu().numpy(), full_g)
+
+
+def test_store_every_scale_and_mantissa():
+    """Groups whose largest magnitude takes every bf16 mantissa at 60 exponents, with ties and neighbours of every border
+    of both roundings among them, byte for byte."""
+    m = torch.arange(128, 256, device=DEV, dtype=torch.float64)
+    e = torch.arange(-34, 26, device=DEV, dtype=torch.float64)
+    top = (m[None] * 2.0 ** e[:, None]).reshape(-1)              # 7680 groups
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    rest = torch.randint(0, 256, (top.numel(), 15), generator=g, device=DEV).double() / 256 * top[:, None]
+    rest *= torch.randint(0, 2, rest.shape, generator=g, device=DEV) * 2 - 1
+    x = torch.cat([top[:, None], rest], 1).to(torch.bfloat16).view(-1, 4, 128)
+    n = x.shape[0]
+    for S in (1.0, 2.0 ** -7, 2.0 ** 40, 2.0 ** -40):
+        k, kg, v, vg = _caches(n, 4, 1)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        y = -x
+        lsa.lsa_store_fp4([x], [y], k, kg, v, vg, [S], [S], _prompts([n], [n], n), dev_status=status)
+        assert status.item() == 0
+        for new, code, group in ((x, k, kg), (y, v, vg)):
+            wc, wg, _ = fp4.quantise(new, S)
+            assert np.array_equal(group[0].cpu().numpy(), wg) and np.array_equal(code[0].cpu().numpy(), wc)

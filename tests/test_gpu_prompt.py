@@ -243,3 +243,88 @@ def test_same_bits_every_time():
 def test_a_token_or_two(H, K, rows, lens):
     """Single tokens, a few of them, and among them a sequence of many."""
     Case(H, K, rows, lens, seed=H, gap=3).run().check()
+
+
+@pytest.mark.parametrize("rows,lens", [([300, 40], [300, 2000]), ([1, 1], [3000, 2000]), ([100], [5000]), ([20], [5000])])
+def test_changed_lengths_in_a_captured_call(rows, lens):
+    """A graph whose row offsets, lengths and contents change between replays (within max_len), and whose workspace
+    another captured call uses too: longer and shorter sequences, rows that move from one to the other, none at all."""
+    c = Case(8, 2, rows, lens, seed=5, max_len=max(lens) + 900)
+    other = Case(8, 2, [1], [4000], seed=6)
+    if other.ws.numel() > c.ws.numel():
+        c.ws = torch.empty_like(other.ws)
+    other.ws = c.ws
+    c.run()
+    other.run()
+    g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="thread_local"):
+        c.run()
+    with torch.cuda.graph(g2, capture_error_mode="thread_local"):
+        other.run()
+    n, b = c.n, len(rows)
+    for new_rows, new_lens in ((rows, lens), ([n] + [0] * (b - 1), [lens[0]] + [0] * (b - 1)),
+                               ([n - (b - 1)] + [1] * (b - 1), [max(lens[0] - 700, n)] + [1] * (b - 1)),
+                               ([0] * b, [0] * b)):
+        c.rows, c.lens = new_rows, new_lens
+        c.ro = np.concatenate([[0], np.cumsum(new_rows)]).tolist()
+        for t, x in ((c.pr.row_offset, c.ro), (c.pr.seq_lens, new_lens)):
+            t.copy_(torch.tensor(x, dtype=torch.int32, device=DEV))
+        c.q.copy_(_rand((n, 8, 128), sum(new_lens)))
+        c.out.fill_(9.0)
+        g.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        skip = [i for i, (r, m) in enumerate(zip(new_rows, new_lens)) if r > m]  # more rows than tokens: refused
+        assert c.status.item() == (lsa.LSA_DEV_BAD_LENGTH if skip else 0)
+        c.status.zero_()
+        c.check(skip)
+        other.check()
+        assert all((c.out[c.ro[i]:c.ro[i + 1]] == 9).all() for i in skip) and (c.out[c.ro[-1]:] == 9).all()
+
+
+@pytest.mark.parametrize("rows,lens", [([1, 2], [4000, 1500]), ([200, 7], [900, 300]), ([20], [4000])])
+def test_far_rows(rows, lens):
+    """Cache rows whose offsets pass 2^32 elements."""
+    c = Case(8, 4, rows, lens, seed=2).run()
+    near, lse = c.out.clone(), c.lse.clone()
+    far = (1 << 23) + 77  # 512 elements a row
+    T = far + c.total
+    for name in ("k", "v"):
+        x = torch.zeros((T, 4, 128), dtype=torch.bfloat16, device=DEV)
+        x[far:] = getattr(c, name)
+        setattr(c, name, x)
+    c.pr = lsa.Prompts(c.pr.row_offset, c.pr.kv_offset + far, c.pr.seq_lens, c.n, c.pr.max_len, T)
+    c.run()
+    assert c.status.item() == 0 and torch.equal(c.out, near) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("rows,lens", [([60, 90, 1], [500, 500, 500]), ([1, 1, 2], [800, 800, 801])])
+def test_sequences_over_the_same_tokens(rows, lens):
+    """Sequences that share one cache range."""
+    c = Case(8, 2, rows, lens, seed=3)
+    c.pr.kv_offset.zero_()
+    c.ko = [0] * len(rows)
+    c.run().check()
+
+
+@pytest.mark.parametrize("H,K,rows,lens,max_len", [
+    (4096, 64, [3, 1], [3, 40], None), (4096, 64, [1], [300], None), (256, 256, [5], [70], None),
+    (8, 1, [40, 3], [40, 90], 1 << 20), (8, 1, [1, 1], [5, 90], 1 << 20), (8, 1, [20], [200], 1 << 20),  # a loose bound
+])
+def test_extents(H, K, rows, lens, max_len):
+    Case(H, K, rows, lens, seed=1, max_len=max_len).run().check()
+
+
+def test_more_sequences_than_a_grid_axis_holds():
+    n = 70000
+    c = Case(2, 1, [1] * n, [1 + i % 3 for i in range(n)], seed=4).run()
+    assert c.status.item() == 0
+    lens, ko = np.array(c.lens), np.array(c.ko)
+    k, v = (torch.zeros((n, 3, 128), dtype=torch.float64, device=DEV) for _ in range(2))
+    seen = torch.tensor(np.arange(3)[None] < lens[:, None], device=DEV)
+    at = torch.tensor(np.minimum(ko[:, None] + np.arange(3)[None], c.total - 1), device=DEV)
+    k[seen], v[seen] = c.k[:, 0][at[seen]].double(), c.v[:, 0][at[seen]].double()
+    z = torch.einsum("nhd,ntd->nht", c.q.double(), k) / 128 ** 0.5
+    p = torch.softmax(z.masked_fill(~seen[:, None], -torch.inf), -1)
+    err = (c.out.double() - torch.einsum("nht,ntd->nhd", p, v)).abs().amax((1, 2))
+    assert (err <= MAX * v.abs().amax((1, 2))).all()
