@@ -1015,7 +1015,7 @@ int32_t lsa_attend_prompt_launches(const lsa_prompts_t* prompts, int32_t H_q, in
     if (prompts == nullptr || prompts->n_seq < 1 || prompts->n_rows < 1 || prompts->max_len < 1 ||
         !prompt_shape_ok(H_q, H_kv, d))
         return 0;
-    return prompt_plan(prompts, H_q, H_kv).n_parts > 1 ? 2 : 1;
+    return prompt_plan(prompts, H_q, H_kv).ws_bytes > 0 ? 2 : 1;
 }
 
 lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
@@ -1048,7 +1048,7 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     a.v = v;
     a.out = out;
     a.lse = lse;
-    if (p.n_parts > 1) {
+    if (p.ws_bytes > 0) {
         a.part_o = static_cast<float*>(workspace);
         a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.off_ml);
     }

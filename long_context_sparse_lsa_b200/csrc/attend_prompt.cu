@@ -46,6 +46,7 @@
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
 #include "internal.h"
+#include "prompt_parts.cuh"
 #include "tcgen05.cuh"
 
 namespace lsa {
@@ -771,15 +772,23 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     // at least (so that long and short ones even out), 128 at most, and 128
     // keys a part. 16 single tokens over up to 3136 tokens, 32/4 heads: 16 us
     // there, 31 us here; 64 over up to 8000: 89 and 201 us.
+    // Up to eight parts are joined in a cluster where all clusters run at once (16
+    // tokens over up to 500: 6.5 us, with the merge kernel 7.9; where they do not,
+    // finished CTAs wait in the way of others: 64 tokens over up to 500 22.5 and
+    // 16.7 us; 9 over up to 1000, eight parts on 97% of the places, 9.8 and 8.2),
+    // and parts of up to 256 keys are taken for that (4 over up to 2000: 7.0
+    // against 8.6 us).
     p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65535;
     if (p.few) {
         const int64_t units = (int64_t)n_seq * H_kv;
         int64_t parts = (2 * (int64_t)num_sms + units - 1) / units;
+        auto at_once = [&](int64_t n) { return 4 * units * n <= 7 * (int64_t)num_sms; };  // 7 of 8 places: a cluster lies within one GPC
+        if (parts > kFewJoined && max_len <= 256 * kFewJoined && at_once(kFewJoined)) parts = kFewJoined;
         parts = parts < 4 ? 4 : parts > 128 ? 128 : parts;
         p.part_keys = (int)((((int64_t)max_len + parts - 1) / parts + 63) / 64 * 64);
         if (p.part_keys < 128) p.part_keys = 128;
         p.n_parts = (int)(((int64_t)max_len + p.part_keys - 1) / p.part_keys);
-        workspace();
+        if (p.n_parts > kFewJoined || !at_once(p.n_parts)) workspace();
         return p;
     }
     // Few rows a sequence: one row tile holds them, and a CTA's second tile
@@ -829,7 +838,7 @@ cudaError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& p, cudaS
         if (e != cudaSuccess) return e;
         e = launch_pdl(attend_prompt_kernel, dim3((unsigned)p.n_items), dim3(kPrThreads), kPrSmem, stream, 0, args);
     }
-    if (e != cudaSuccess || p.n_parts == 1) return e;
+    if (e != cudaSuccess || p.ws_bytes == 0) return e;
     const int per = p.n_parts <= 8 ? 1 : p.n_parts <= 16 ? 2 : p.n_parts <= 32 ? 4 : 8;  // eight parts in flight a warp
     const int64_t blocks = ((int64_t)a.n_rows * a.H_q + kPmWarps / per - 1) / (kPmWarps / per);
     return launch_pdl(prompt_merge_kernel, dim3((unsigned)blocks), dim3(kPmWarps * kWarp), 0, stream, 0, a, per);

@@ -13,11 +13,15 @@
 // the keys as M and the sequence's (row, query head) pairs as N columns, mma
 // m16n8k16 in bf16, online softmax in fp32, O^T += V^T P^T with P^T as bf16
 // through movmatrix. The warps merge through shared memory; the parts of a row
-// are combined by prompt_merge_kernel. A part has a fixed number of keys, so
-// that CTAs are alike whatever the sequences' lengths; those behind a
-// sequence's end have nothing to do.
+// are combined by prompt_merge_kernel, or, where few of them run at once
+// (plan_prompt), are a cluster's CTAs that join their results through
+// distributed shared memory (16 tokens over up to 500: 6.5 against 7.9 us). A
+// part has a fixed number of keys, so that CTAs are alike whatever the
+// sequences' lengths; those behind a sequence's end have nothing to do. In a
+// cluster it is an equal share of its sequence.
 #include "common.cuh"
 #include "internal.h"
+#include "prompt_parts.cuh"
 
 namespace lsa {
 namespace {
@@ -28,7 +32,10 @@ constexpr int kFwRow = kFwD * 2;                       // bytes of a K or V row
 constexpr int kFwTileBytes = 2 * kFwTile * kFwRow;     // K, then V: 8 KB
 constexpr int kFwSmem = kFwWarps * kFwRing * kFwTileBytes;
 constexpr int kFwPark = 36;                            // floats of a lane per column tile: o, m, l
-static_assert(kFwWarps * 4 * kFwPark * kWarp * 4 <= kFwSmem, "the merge area lies in the rings");
+constexpr int kFwJoinRow = kFwD + 4;                   // floats of a column in the cluster's merge area (padded: no bank conflicts)
+// the merge areas lie in the rings: the warps' results, then the CTA's
+__host__ __device__ constexpr int fw_join_at(int nt) { return kFwWarps * nt * kFwPark * kWarp * 4; }
+static_assert(fw_join_at(2) + 16 * (kFwJoinRow * 4 + 8) <= kFwSmem, "shared memory of one CTA");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -39,8 +46,9 @@ __device__ __forceinline__ float ex2(float x) {
 // 16-byte chunk c of row m, so that eight rows' equal chunks fall on all banks.
 __device__ __forceinline__ uint32_t fw_at(int m, int c) { return (uint32_t)(m * kFwRow + 16 * (c ^ (m & 7))); }
 
-// NT: tiles of 8 (row, query head) columns taken at a time.
-template <int NT>
+// NT: tiles of 8 (row, query head) columns taken at a time. JOINED: the parts
+// of a sequence are a cluster.
+template <int NT, bool JOINED>
 __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const __grid_constant__ PromptArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
@@ -56,9 +64,11 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
         return;
     }
     const int base = len - n;                     // tokens before the first row
-    const int k_lo = part * a.part_keys, k_hi = min(len, k_lo + a.part_keys);
-    if (k_lo >= len) return;
-    const int n_tiles = (k_hi - k_lo + kFwTile - 1) / kFwTile;
+    // (a cluster's parts are equal shares of the sequence)
+    const int part_keys = JOINED ? ((len + a.n_parts - 1) / a.n_parts + kFwTile - 1) / kFwTile * kFwTile : a.part_keys;
+    const int k_lo = min(len, part * part_keys), k_hi = min(len, k_lo + part_keys);
+    if (!JOINED && k_lo >= len) return;
+    const int n_tiles = max(0, k_hi - k_lo + kFwTile - 1) / kFwTile;
     const int G = a.G, cols = n * G;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFwRing * kFwTileBytes);
     const uint16_t* kb = a.k + off * a.k_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
@@ -82,6 +92,8 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
 
     for (int c0 = 0; c0 < cols; c0 += 8 * NT) {
         if (c0 > 0) __syncthreads();  // the merge area of the columns before
+        float* join = reinterpret_cast<float*>(smem + fw_join_at(NT));  // [column][kFwJoinRow], then [column] (m, l)
+        float2* join_ml = reinterpret_cast<float2*>(join + 8 * NT * kFwJoinRow);
 #pragma unroll
         for (int j = 0; j < kFwRing - 1; ++j) fetch(warp + j * kFwWarps, j);
         // query fragments, and the keys that the lane's accumulator columns see
@@ -258,6 +270,13 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
 #pragma unroll
                     for (int q = 0; q < 4; ++q) y[q] += x[(4 * (2 * warp + (q >> 1)) + c + 2 * (q & 1)) * kWarp] * f;
                 }
+                if (JOINED) {
+                    const int own = 8 * t + 2 * t4 + c;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) join[own * kFwJoinRow + 16 * (2 * warp + (q >> 1)) + 8 * (q & 1) + g] = y[q];
+                    if (warp == 0 && g == 0) join_ml[own] = make_float2(l == 0.f ? M : fmaxf(M, -3e38f), l);
+                    continue;
+                }
                 if (col >= cols) continue;
                 const int64_t row = (int64_t)(row0 + col / G) * a.H_q + kvh * G + col % G;
                 // channels 16 mt + g and + 8 of mt = 2 warp, 2 warp + 1
@@ -278,19 +297,61 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
                         reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(l == 0.f ? M : fmaxf(M, -3e38f), l);
                 }
             }
+        if (!JOINED) continue;
+        // ---- the cluster's parts: each CTA combines its share of (column, 4 channels) ------------
+        __syncwarp();
+        cluster_sync();
+        for (int e = part * kFwThreads + tid; e < 8 * NT * (kFwD / 4); e += a.n_parts * kFwThreads) {
+            const int own = e / (kFwD / 4), ch = 4 * (e % (kFwD / 4)), col = c0 + own;
+            if (col >= cols) continue;
+            float2 ml[kFewJoined];
+            float4 v[kFewJoined];
+            float M = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < kFewJoined; ++p) {
+                ml[p] = make_float2(-INFINITY, 0.f);
+                v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p < a.n_parts) {
+                    ml[p] = ld_cluster_f2(map_cta(smem_u32(&join_ml[own]), (uint32_t)p));
+                    v[p] = ld_cluster_f4(map_cta(smem_u32(&join[own * kFwJoinRow + ch]), (uint32_t)p));
+                }
+                M = fmaxf(M, ml[p].x);
+            }
+            float l = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < kFewJoined; ++p) {
+                if (ml[p].x == -INFINITY) continue;  // no keys
+                const float f = ex2(ml[p].x - M);
+                l += ml[p].y * f;
+                y.x += v[p].x * f;
+                y.y += v[p].y * f;
+                y.z += v[p].z * f;
+                y.w += v[p].w * f;
+            }
+            const int64_t row = (int64_t)(row0 + col / G) * a.H_q + kvh * G + col % G;
+            const float inv = 1.f / l;
+            *reinterpret_cast<uint2*>(a.out + row * kFwD + ch) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+            if (a.lse != nullptr && ch == 0) a.lse[row] = (M + log2f(l)) * 0.6931471805599453f;
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA reads another's shared memory after this
     }
 }
 
 }  // namespace
 
 cudaError_t launch_attend_prompt_few(const PromptArgs& a, int parts, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed[2];
+    static std::atomic<uint64_t> allowed[4];
     // columns of most sequences: 8 or fewer (one token of up to 8 heads), or more
     const bool wide = (int64_t)a.n_rows * a.G > (int64_t)a.n_seq * 8;
-    auto kern = wide ? attend_prompt_few_kernel<2> : attend_prompt_few_kernel<1>;
-    const cudaError_t e = allow_smem(kern, kFwSmem, allowed[wide ? 1 : 0]);
+    const bool joined = parts > 1 && a.part_o == nullptr;
+    auto kern = wide ? (joined ? attend_prompt_few_kernel<2, true> : attend_prompt_few_kernel<2, false>)
+                     : (joined ? attend_prompt_few_kernel<1, true> : attend_prompt_few_kernel<1, false>);
+    const cudaError_t e = allow_smem(kern, kFwSmem, allowed[wide + 2 * joined]);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)parts, (unsigned)a.H_kv, (unsigned)a.n_seq), dim3(kFwThreads), kFwSmem, stream, 0, a);
+    return launch_pdl(kern, dim3((unsigned)parts, (unsigned)a.H_kv, (unsigned)a.n_seq), dim3(kFwThreads), kFwSmem, stream,
+                      joined ? parts : 0, a);
 }
 
 }  // namespace lsa

@@ -239,13 +239,13 @@ def test_same_bits_every_time():
 
 @pytest.mark.parametrize("H,K", [(8, 1), (16, 1), (32, 4), (4, 4), (6, 2), (64, 1), (40, 2)])
 @pytest.mark.parametrize("rows,lens", [([1] * 5, [1, 2, 17, 640, 3001]), ([2, 1, 0, 1], [2, 900, 40, 64]), ([1, 40, 1, 1], [700, 100, 65, 64]),
-                                       ([1] * 70, [64 + 9 * i for i in range(70)])])
+                                       ([1] * 70, [64 + 9 * i for i in range(70)]), ([1, 1, 2], [1000, 3, 129]), ([3, 0], [1500, 0])])
 def test_a_token_or_two(H, K, rows, lens):
     """Single tokens, a few of them, and among them a sequence of many."""
     Case(H, K, rows, lens, seed=H, gap=3).run().check()
 
 
-@pytest.mark.parametrize("rows,lens", [([300, 40], [300, 2000]), ([1, 1], [3000, 2000]), ([100], [5000]), ([20], [5000])])
+@pytest.mark.parametrize("rows,lens", [([300, 40], [300, 2000]), ([1, 1], [3000, 2000]), ([1, 1], [900, 600]), ([100], [5000]), ([20], [5000])])
 def test_changed_lengths_in_a_captured_call(rows, lens):
     """A graph whose row offsets, lengths and contents change between replays (within max_len), and whose workspace
     another captured call uses too: longer and shorter sequences, rows that move from one to the other, none at all."""

@@ -36,7 +36,8 @@ def test_refuses_before_launch(kw, want):
 def test_workspace_and_launches_follow_the_splits():
     lib = lsa.load_library()
     for n_seq, n_rows, max_len, split in [(1, 1, 9000, True), (1, 8000, 9000, False), (16, 16, 3136, True), (64, 64, 9000, True),
-                                          (1, 1, 100, False)]:
+                                          (1, 1, 100, False), (4, 40, 9000, True),
+                                          (16, 16, 1000, False), (4, 4, 2000, False), (9, 9, 2000, True)]:  # joined in clusters
         p = _prompts(n_seq=n_seq, n_rows=n_rows, max_len=max_len)
         assert lib.lsa_attend_prompt_launches(p, 32, 4, 128) == (2 if split else 1)
         assert (lib.lsa_attend_prompt_workspace_size(p, 32, 4, 128) > 0) == split
