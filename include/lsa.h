@@ -541,10 +541,11 @@ lsa_status_t lsa_attend_si(const uint16_t *const *q, const uint16_t *const *k_ca
  * out      device bf16 [n_rows][H_q][d].
  * lse      device fp32 [n_rows][H_q] or NULL: ln sum_j exp(q . k_j / sqrt(d)).
  * workspace lsa_attend_prompt_workspace_size() bytes (partials of few rows over
- *          long caches; no initialisation needed; may be NULL when that is 0).
+ *          long caches, depending on n_seq, n_rows and max_len; no initialisation
+ *          needed; may be NULL when that is 0).
  * All device pointers 16-byte aligned (out 32, lse 4). Supported: d == 128; H_q / H_kv
  * a whole number up to 64; H_q <= 4096; n_rows * H_q < 2^31. One launch, plus
- * a merge when the keys are split.
+ * a merge where the workspace size is not 0.
  */
 size_t lsa_attend_prompt_workspace_size(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
 int32_t lsa_attend_prompt_launches(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
