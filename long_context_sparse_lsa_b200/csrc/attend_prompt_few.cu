@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
             slot = slot + 1 == kFwRing ? 0 : slot + 1;
             const int key0 = k_lo + i * kFwTile;
             const bool masked = key0 + kFwTile > base + 1;  // some column does not see some key of the tile
+            bool odd = false;  // some element under the mask is not finite
             if (masked && n > 1) {
                 // V of the newest tokens: rows before them have weight 0, and 0 times an
                 // element that is not finite is not 0: such elements are zeroed here and
@@ -149,8 +150,9 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
                         e[q] &= ~(((bad >> 15) & 0x00010001u) * 0xffffu);
                     }
                     if (any) st_shared_v4(at, y.x, y.y, y.z, y.w);
+                    odd |= any != 0;
                 }
-                __syncwarp();
+                odd = __any_sync(0xffffffffu, odd);
             }
             // ---- S^T: 16 keys x 8 NT columns ------------------------------------------------
             float s[NT][4];
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma_bf16(o[t][mt], fr, p[t][0], p[t][1]);
             }
-            if (masked && n > 1) {
+            if (odd) {
                 for (int m = max(0, base + 1 - key0); m < kFwTile && key0 + m < k_hi; ++m) {
                     const uint16_t* v = a.v + (off + key0 + m) * a.v_stride + (int64_t)kvh * kFwD;
                     for (int mt = 0; mt < 8; ++mt)
