@@ -164,7 +164,8 @@ def test_rows_behind_and_other_sequences_hold_anything():
     assert (c.out[100:130].double() - full[100:130].double()).abs().max() <= 2 * MAX * 5
 
 
-@pytest.mark.parametrize("H,K,n,length", [(8, 1, 300, 300), (1, 1, 700, 800), (8, 1, 1, 4000), (64, 1, 9, 200)])
+@pytest.mark.parametrize("H,K,n,length", [(8, 1, 300, 300), (1, 1, 700, 800), (8, 1, 1, 4000), (64, 1, 9, 200),
+                                          (4, 1, 3, 200), (1, 1, 16, 30), (2, 1, 8, 2500)])
 def test_not_finite_where_it_is_seen(H, K, n, length):
     """A K or V that is not finite reaches the rows that see it and no other."""
     for where in (length - 1, max(0, length - n // 2 - 1), length - n):
@@ -328,3 +329,22 @@ def test_more_sequences_than_a_grid_axis_holds():
     p = torch.softmax(z.masked_fill(~seen[:, None], -torch.inf), -1)
     err = (c.out.double() - torch.einsum("nht,ntd->nhd", p, v)).abs().amax((1, 2))
     assert (err <= MAX * v.abs().amax((1, 2))).all()
+
+
+@pytest.mark.parametrize("H,K,rows,lens", [(4, 1, [3, 1, 1], [200, 5, 70]), (1, 1, [16, 1, 2], [30, 40, 9]), (2, 1, [8, 1], [2500, 30]),
+                                           (16, 2, [2, 2, 1], [900, 2, 600])])
+def test_not_finite_with_a_few_rows(H, K, rows, lens):
+    n, length, h = rows[0], lens[0], H // K
+    for where in (length - 1, length - n // 2, length - n, length - n - 1):
+        c = Case(H, K, rows, lens, seed=6, gap=2)
+        at = c.ko[0] + where
+        c.v[at, 0, 5], c.v[at, 0, 77], c.v[at, 0, 127] = float("inf"), float("nan"), float("-inf")
+        c.v[c.ko[0] + length:c.ko[0] + length + 2] = float("nan")  # behind the sequence: of nobody
+        c.run().check()
+        c = Case(H, K, rows, lens, seed=7)
+        c.k[where, 0, 5] = float("nan")
+        c.run().check()
+    c = Case(H, K, rows, lens, seed=8)
+    c.q[n - 1, 0, 3] = float("nan")
+    c.run().check()
+    assert c.out[n - 1, :h].isnan().any()
