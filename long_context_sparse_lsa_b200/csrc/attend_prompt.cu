@@ -346,13 +346,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 ++handed;
             };
             for (int i = (int)blockIdx.x; ok && i >= 0;) {
-                if (lane == 0) {  // the item after this one
-                    mbar_arrive_expect_tx(smem_u32(&sh.answer_full), 16);
-                    try_cancel(smem_u32(sh.answer), smem_u32(&sh.answer_full));
-                }
-                ++asked;
                 const PrItem it = pr_item(a, i, true);
                 if (it.live) hand_out(it);
+                // The item after this one is asked for with this one's last two key tiles: a
+                // CTA that asks at an item's start takes items that idle ones could start on
+                // (24 chunks of up to 527 rows, 8/4 heads: 94 us, so 68).
+                auto ask = [&]() {
+                    mbar_arrive_expect_tx(smem_u32(&sh.answer_full), 16);
+                    try_cancel(smem_u32(sh.answer), smem_u32(&sh.answer_full));
+                    ++asked;
+                };
+                if (lane == 0 && ok && !(it.live && it.n > 0)) ask();
                 if (lane == 0 && it.live) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
@@ -367,6 +371,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                                         smem_u32(&sh.q_full[w]));
                     }
                     for (int i = 0; ok && i < 2 * it.n; ++i) {
+                        if (i == max(0, 2 * it.n - 4)) ask();
                         const int st = loads % kPrStages;
                         if (loads >= kPrStages && !pr_wait(sh, sh.empty[st], (loads / kPrStages + 1) & 1, a.dev_status))
                             ok = false;
@@ -381,6 +386,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, (int)(ok && !pr_aborted(sh)), 0) != 0;
+                asked = __shfl_sync(0xffffffffu, asked, 0);
                 ok = ok && __all_sync(0xffffffffu, pr_wait(sh, sh.answer_full, (uint32_t)(asked - 1) & 1u, a.dev_status));
                 if (ok) i = cancelled_cta(smem_u32(sh.answer));
                 fence_proxy_async_smem();
@@ -798,19 +804,28 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     const int tc = p.dual ? p.tile_tokens : 2 * p.tile_tokens;
     const int64_t slots = n_rows / tc + n_seq;
     const int64_t items = (((int64_t)n_rows + tc - 1) / tc + (n_seq - 1) / 2) * H_kv;  // about those with rows
-    // Key splits: as many as give the shortest of (rounds of items over the
-    // SMs) x (key tiles of an item, with its start and end) + the merge, in us:
-    // a step of both tiles takes about 1.7, an item's start and end 5, a row's
-    // partials are written and read at about 4 TB/s.
+    // Key splits: as many as give the shortest of (the longest item, or all items
+    // over the SMs and the end of the last ones) + the merge, in us: a step of both
+    // tiles takes about 1.7, an item's start and end 5, a row's partials are written
+    // and read at 2.5 TB/s. At 32/4 heads, measured for 1, 2 and more splits: 353
+    // rows each on 15868 tokens, two sequences 218, 129, 137 us (3); 60 each on
+    // 8060, four 115, 67, 36 (6), 34 us (8); 3000-token prompts 77 and 161 us.
     const int64_t keys = max_len - (n_rows / n_seq) / 2 > kPrKeys ? max_len - (n_rows / n_seq) / 2 : kPrKeys;
+    const double tiles = (double)key_tiles / (p.dual ? 2 : 1);
     const double steps = (double)((keys + kPrKeys - 1) / kPrKeys) / (p.dual ? 2 : 1);
     double best = 0;
     p.n_splits = 1;
     for (int s = 1; s <= 64 && s <= key_tiles; ++s) {
-        const int64_t rounds = (items * s + num_sms - 1) / num_sms;
         const int parts = p.dual ? 2 * s : s;
-        const double merge = parts > 1 ? 3 + 2.0 * parts * n_rows * H_q * 520 / 4e6 : 0;
-        const double t = (double)rounds * (1.7 * (double)((int64_t)(steps / s) + 1) + 5) + merge;
+        const double longest = 1.7 * (tiles / s + 0.5) + 5, mean = 1.7 * (steps / s + 0.5) + 5;
+        double t = longest;
+        if (items * s > num_sms) {
+            // the last round is full or empty where items are alike, else short items even it out
+            const int64_t rounds = (items * s + num_sms - 1) / num_sms;
+            const double all = mean > 0.9 * longest ? (double)rounds * mean : ((double)(items * s) / num_sms + 0.3) * mean;
+            if (all > t) t = all;
+        }
+        if (parts > 1) t += 3 + 2.0 * parts * n_rows * H_q * 520 / 2.5e6;
         if (s == 1 || t < 0.97 * best) {
             best = t;
             p.n_splits = s;
