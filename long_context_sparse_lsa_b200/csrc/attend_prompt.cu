@@ -40,8 +40,8 @@
 //  * What bounds it: the chain of one row tile, softmax (1950 cycles), P V (512),
 //    the next S (512) and their hand-overs (350), whose tensor part the other row
 //    tile's fills to 61%; with long prompts the board's power as well (1.6 to
-//    1.7 GHz): 16384 tokens, 32/4 heads, 1130 TFLOP/s. Short prompts (24 of up to
-//    1500 tokens: 650 TFLOP/s) add 8000 cycles an item for the first S, the
+//    1.7 GHz): 16384 tokens, 32/4 heads, 1140 TFLOP/s. Short prompts (24 of up to
+//    1500 tokens: 640 TFLOP/s) add 8000 cycles an item for the first S, the
 //    masked tile and the output.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
@@ -133,9 +133,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // P of 32 scores as bf16 pairs, and their sum onto sum[0..1]: 2^(z c - mc),
-// kPoly of the 16 pairs on the FMA units, beside the special-function unit, whose 16 results a clock and SM are half of what the tensor
-// core's tiles ask for (128 columns of one warp a scheduler: 1519 cycles
-// without, 967 with 6 pairs of 16, 1217 with 8). A NaN may come out as a number.
+// kPoly of the 16 pairs on the FMA units, beside the special-function unit, whose
+// 16 results a clock and SM are half of what the tensor core's tiles ask for. One
+// warp a scheduler alone is fastest with 6 pairs (128 columns 967 cycles, 1519
+// without, 1217 with 8); two, in the whole kernel, with 4: 16384 tokens, 32/4
+// heads 1933 us with 2, 1916 with 4, 1950 with 6, 2100 with 8. A NaN may come out
+// as a number.
 // 2^x: x = n + f with n = floor(x) (adding 1.5 * 2^23 rounded down leaves n in
 // the low bits), 2^f on [0, 1) by the polynomial of degree 4 with the smallest
 // largest relative error (3e-6) among those that are 1 at 0 (fitted by
@@ -143,7 +146,7 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 // -127, for which the bits are those of 0. The pairs go through it stage by
 // stage, with a few of the others' exponentials between the stages: in
 // program order pair by pair the same takes 2021 cycles.
-constexpr int kPoly = 6;
+constexpr int kPoly = 4;
 __device__ __forceinline__ void exp_split(const float (&z)[32], f32x2 c, f32x2 neg_mc, f32x2 (&sum)[2], uint32_t* p) {
     constexpr int kRest = 16 - kPoly, kStages = 7;
     const f32x2 big = pair(12582912.f, 12582912.f), neg_big = pair(-12582912.f, -12582912.f), minus = pair(-1.f, -1.f);
