@@ -181,9 +181,9 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
     const uint32_t s_off = (uint32_t)((HPC > 1 && lane >= 16 ? kVScales : kKScales) + sm * HPC * 8 + kSBytes * (lane % kSChunks));
     auto fetch = [&](int entries, uint32_t slot) {
         const uint32_t to = ring + slot;
-        const bool whole = __all_sync(0xffffffffu, entries >= 0);
+        const uint32_t there = __ballot_sync(0xffffffffu, entries >= 0);
         const uint32_t clamped = (uint32_t)max(entries, 0);
-        if (whole) {
+        if (there == 0xffffffffu) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const uint32_t e = __shfl_sync(0xffffffffu, clamped, h_local * kTokens + (32 * x + lane) / kChunks);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
             } else {
                 cp_async_full16(to + s_off, sc0 + (uint64_t)e * s_row);
             }
-        } else {  // a missing entry's bytes are zeros
+        } else if (there != 0u) {  // a missing entry's bytes are zeros (a step without entries is not looked at)
 #pragma unroll 1
             for (int x = 0; x < 4; ++x) {
                 const int m = h_local * kTokens + (32 * x + lane) / kChunks;
