@@ -41,8 +41,8 @@
 //  * What bounds it: where every SM has a CTA with many steps, the instructions
 //    (a step of a head is about 650; 61% of the issue slots, the integer pipe
 //    with the conversions 51%): 64 rows of 3136 entries, two layers: 68 us, 235
-//    MB at 3.4 TB/s, on 128 of 148 SMs. With few rows the chain of row lookup,
-//    set, gather, products and merge: 12 us for one row of four layers.
+//    MB at 3.5 TB/s, on 128 of 148 SMs. With few rows the chain of row lookup,
+//    set, gather, products and merge: 11 us for one row of four layers.
 #include "fp4.cuh"
 #include "internal.h"
 
@@ -497,7 +497,8 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
     // 16 query heads), a CTA's start and end 6, a merge 3 and a little per split.
     // At 3136 entries, 32/4 heads, measured for each count of splits (1, 3, the
     // chosen one): 4 rows 65, 29, 12 us (37 splits); 16 rows 65, 29, 17 (9);
-    // 80 rows 67, 60, 60; 128 rows 69, 87, 69 (1); 163 rows 133, 112, 112.
+    // 80 rows 67, 60, 60; 128 rows 69, 87, 69 (1); 163 rows 133, 112, 112. (Before
+    // steps without entries were skipped, which took about 1 us off each.)
     const double round = H_q / H_kv > 8 ? 2.0 : 2.5;
     int per = steps > 0 ? steps : 1;
     double best = 0;
