@@ -502,8 +502,11 @@ AttendPlan plan_attend_fp4(int n_q, int H_q, int H_kv, int budget, int G, int nu
     const double round = H_q / H_kv > 8 ? 2.0 : 2.5;
     int per = steps > 0 ? steps : 1;
     double best = 0;
-    for (int s = 1; s <= 64 && s <= steps; ++s) {
-        const int each = (steps + s - 1) / s, parts = (steps + each - 1) / each;
+    for (int s = 1, last = 0; s <= 64 && s <= steps; ++s) {
+        const int each = (steps + s - 1) / s;
+        if (each == last) continue;  // (no more splits than before)
+        last = each;
+        const int parts = (steps + each - 1) / each;
         const long waves = (units * parts + num_sms - 1) / num_sms;
         const double t = (double)waves * (round * ((each + n_sel - 1) / n_sel) + 6) + (parts > 1 ? 3 + 0.03 * parts : 0);
         if (s == 1 || t < 0.97 * best) {
