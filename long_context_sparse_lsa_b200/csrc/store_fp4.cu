@@ -20,10 +20,10 @@
 // in a tie.
 //
 // Bound: HBM bytes (2 read, 9/16 written per number, 2 more with the rounded
-// rows: 306 MB for 65536 tokens of 4 heads, 52 us); with a few rows, the latency
+// rows: 306 MB for 65536 tokens of 4 heads, 49 us); with a few rows, the latency
 // of the dependent loads. With an IEEE division and reciprocal per group, a
 // 64-bit division per thread and seven operations per number the instructions
-// bound it (85% of the issue slots, 56 us). One thread per group: 32 bytes in, 8
+// bound it (85% of the issue slots, 56 us). A thread per group or two: 32 bytes in, 8
 // code bytes and 1 scale byte out, consecutive threads on consecutive groups,
 // so that every access of a warp is a run.
 #include "fp4.cuh"
@@ -101,31 +101,42 @@ __device__ __forceinline__ void quantise(const Groups16& in, float S, float inv_
     }
 }
 
-// grid: (runs of kStThreads groups, layers * 2): K of layer g at y = 2 g, V at 2 g + 1
-template <bool VALUES>
+// grid: (runs of PER * kStThreads groups, layers * 2): K of layer g at y = 2 g, V
+// at 2 g + 1. A thread takes PER groups, kStThreads apart, all asked for at once.
+template <bool VALUES, int PER>
 __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_constant__ StoreFp4Args a) {
-    __shared__ int64_t s_dst[kStThreads / kFp4Groups + 2];
+    constexpr int kPairs = PER * kStThreads / kFp4Groups;  // (row, head) pairs of a CTA
+    __shared__ int64_t s_dst[kPairs + 2];
     const int tid = threadIdx.x;
     const int layer = blockIdx.y >> 1, is_v = blockIdx.y & 1;
     const int per_row = a.H_kv * kFp4Groups;
-    // the CTA's 32 (row, head) pairs (their number fits 32 bits, as n_rows * H_kv does)
-    const uint32_t pair0 = blockIdx.x * (uint32_t)(kStThreads / kFp4Groups), H = (uint32_t)a.H_kv;
-    const uint32_t first = pair0 / H, head = pair0 - first * H + (uint32_t)(tid / kFp4Groups);
+    // (the number of pairs fits 32 bits, as n_rows * H_kv does)
+    const uint32_t pair0 = blockIdx.x * (uint32_t)kPairs, H = (uint32_t)a.H_kv;
+    const uint32_t first = pair0 / H;
     const int row0 = (int)first;
-    const int row = row0 + (int)(head / H);
-    const int in_row = (int)(head % H) * kFp4Groups + tid % kFp4Groups;
-    const bool live = row < a.n_rows;
+    int row[PER], in_row[PER];
+    Groups16 x[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const uint32_t head = pair0 - first * H + (uint32_t)(u * (kStThreads / kFp4Groups) + tid / kFp4Groups);
+        row[u] = row0 + (int)(head / H);
+        in_row[u] = (int)(head % H) * kFp4Groups + tid % kFp4Groups;
+    }
     pdl_enter();
-    Groups16 x = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (live) {
-        const uint16_t* src = (is_v ? a.v_new[layer] : a.k_new[layer]) + (int64_t)row * (is_v ? a.v_stride : a.k_stride) +
-                              in_row * kFp4Group;
-        x.a = *reinterpret_cast<const uint4*>(src);
-        x.b = *reinterpret_cast<const uint4*>(src + 8);
+    const uint16_t* src = is_v ? a.v_new[layer] : a.k_new[layer];
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        x[u] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (row[u] < a.n_rows) {
+            const uint16_t* p = src + (int64_t)row[u] * stride + in_row[u] * kFp4Group;
+            x[u].a = *reinterpret_cast<const uint4*>(p);
+            x[u].b = *reinterpret_cast<const uint4*>(p + 8);
+        }
     }
     // cache rows of the CTA's tokens
     if (tid < kWarp) {
-        const int last = min(a.n_rows - 1, (int)((pair0 + kStThreads / kFp4Groups - 1) / H));
+        const int last = min(a.n_rows - 1, (int)((pair0 + kPairs - 1) / H));
         int seq = find_last(a.n_seq, [&](int b) { return a.row_offset[b] <= row0; });
         for (int i = tid; i <= last - row0; i += kWarp) {
             const int r = row0 + i;
@@ -144,23 +155,26 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
             s_dst[i] = dst;
         }
     }
-    GroupFp4 q;
     const float S = is_v ? a.v_scale[layer] : a.k_scale[layer];
-    quantise<VALUES>(x, S, 1.f / S, q);
     __syncthreads();
-    if (!live) return;
-    const int64_t dst = s_dst[row - row0];
-    if (dst < 0) return;
-    if (q.bad) flag(a.dev_status, LSA_DEV_BAD_VALUE);
-    const int64_t to = dst * per_row + in_row;
-    *reinterpret_cast<uint2*>((is_v ? a.v[layer] : a.k[layer]) + to * 8) = make_uint2(q.code[0], q.code[1]);
-    (is_v ? a.v_group[layer] : a.k_group[layer])[to] = (uint8_t)q.scale;
-    if (VALUES) {
-        uint16_t* out = is_v ? a.v_round[layer] : a.k_round[layer];
-        if (out != nullptr) {
-            uint4* p = reinterpret_cast<uint4*>(out + ((int64_t)row * per_row + in_row) * kFp4Group);
-            p[0] = make_uint4(q.value[0], q.value[1], q.value[2], q.value[3]);
-            p[1] = make_uint4(q.value[4], q.value[5], q.value[6], q.value[7]);
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        if (row[u] >= a.n_rows) return;
+        const int64_t dst = s_dst[row[u] - row0];
+        if (dst < 0) continue;
+        GroupFp4 q;
+        quantise<VALUES>(x[u], S, 1.f / S, q);
+        if (q.bad) flag(a.dev_status, LSA_DEV_BAD_VALUE);
+        const int64_t to = dst * per_row + in_row[u];
+        *reinterpret_cast<uint2*>((is_v ? a.v[layer] : a.k[layer]) + to * 8) = make_uint2(q.code[0], q.code[1]);
+        (is_v ? a.v_group[layer] : a.k_group[layer])[to] = (uint8_t)q.scale;
+        if (VALUES) {
+            uint16_t* out = is_v ? a.v_round[layer] : a.k_round[layer];
+            if (out != nullptr) {
+                uint4* p = reinterpret_cast<uint4*>(out + ((int64_t)row[u] * per_row + in_row[u]) * kFp4Group);
+                p[0] = make_uint4(q.value[0], q.value[1], q.value[2], q.value[3]);
+                p[1] = make_uint4(q.value[4], q.value[5], q.value[6], q.value[7]);
+            }
         }
     }
 }
@@ -169,9 +183,17 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
 
 cudaError_t launch_store_fp4(const StoreFp4Args& a, cudaStream_t stream) {
     const int64_t groups = (int64_t)a.n_rows * a.H_kv * kFp4Groups;
-    const dim3 grid((unsigned)((groups + kStThreads - 1) / kStThreads), (unsigned)(2 * a.layers));
-    return launch_pdl(a.values ? store_fp4_kernel<true> : store_fp4_kernel<false>, grid, dim3(kStThreads), 0, stream,
-                      0, a);
+    // Two groups a thread where one each would be more than two rounds of the eight
+    // CTAs that an SM holds: half the searches and more bytes in flight (65536
+    // tokens, 4 heads 48.7 against 52.2 us, 16000 tokens 15.6 and 16.2; 16 tokens
+    // 3.8 and 3.1).
+    const int64_t ctas = (groups + kStThreads - 1) / kStThreads * 2 * a.layers;
+    const bool two = ctas > 16 * (int64_t)device_sm_count();
+    const int per = two ? 2 : 1;
+    auto kern = a.values ? (two ? store_fp4_kernel<true, 2> : store_fp4_kernel<true, 1>)
+                         : (two ? store_fp4_kernel<false, 2> : store_fp4_kernel<false, 1>);
+    const dim3 grid((unsigned)((groups + per * kStThreads - 1) / (per * kStThreads)), (unsigned)(2 * a.layers));
+    return launch_pdl(kern, grid, dim3(kStThreads), 0, stream, 0, a);
 }
 
 }  // namespace lsa

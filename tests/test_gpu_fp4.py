@@ -400,3 +400,29 @@ def test_store_every_scale_and_mantissa():
         for new, code, group in ((x, k, kg), (y, v, vg)):
             wc, wg, _ = fp4.quantise(new, S)
             assert np.array_equal(group[0].cpu().numpy(), wg) and np.array_equal(code[0].cpu().numpy(), wc)
+
+
+@pytest.mark.parametrize("H,G,rows,lens", [(4, 1, [5000, 1, 6999], [5000, 300, 7100]), (3, 2, [4099], [4099]), (256, 1, [301], [400])])
+def test_store_many_rows(H, G, rows, lens):
+    """Enough rows that a thread takes two groups; a last CTA that is not full."""
+    n = sum(rows)
+    total = sum(lens) + 4 * (len(lens) + 1)
+    pr = _prompts(rows, lens, total, 4)
+    k_new, v_new = ([_rand((n, H, 128), 3 * g + i) for g in range(G)] for i in (0, 1))
+    scale = [2.0 ** -g for g in range(G)]
+    k, kg, v, vg = _caches(total, H, G)
+    kr, vr = ([torch.empty((n, H, 128), dtype=torch.bfloat16, device=DEV) for _ in range(G)] for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lsa.lsa_store_fp4(k_new, v_new, k, kg, v, vg, scale, scale, pr, kr, vr, status)
+    again = _caches(total, H, G)
+    lsa.lsa_store_fp4(k_new, v_new, *again, scale, scale, pr)
+    assert status.item() == 0
+    at = np.concatenate([np.arange(o + m - r, o + m) for o, m, r in zip(pr.kv_offset.tolist(), lens, rows)]).astype(int)
+    for new, code, group, rnd, code2, group2 in ((k_new, k, kg, kr, again[0], again[1]), (v_new, v, vg, vr, again[2], again[3])):
+        for g in range(G):
+            wc, wg, wv = fp4.quantise(new[g], scale[g])
+            full_c, full_g = np.full((total, H, 64), 0xA5, np.uint8), np.full((total, H, 8), 0xA5, np.uint8)
+            full_c[at], full_g[at] = wc, wg
+            assert np.array_equal(group[g].cpu().numpy(), full_g) and np.array_equal(code[g].cpu().numpy(), full_c)
+            assert torch.equal(code[g], code2[g]) and torch.equal(group[g], group2[g])
+            assert torch.equal(rnd[g].cpu(), torch.tensor(wv).to(torch.bfloat16))
