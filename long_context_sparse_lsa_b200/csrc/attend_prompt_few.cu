@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
                     odd |= any != 0;
                 }
                 odd = __any_sync(0xffffffffu, odd);
+                __syncwarp();  // (a vote orders no memory: other lanes read what this one has zeroed)
             }
             // ---- S^T: 16 keys x 8 NT columns ------------------------------------------------
             float s[NT][4];

@@ -348,3 +348,21 @@ def test_not_finite_with_a_few_rows(H, K, rows, lens):
     c.q[n - 1, 0, 3] = float("nan")
     c.run().check()
     assert c.out[n - 1, :h].isnan().any()
+
+
+@pytest.mark.parametrize("H,K,n,length", [(8, 1, 2, 40), (1, 1, 16, 64), (2, 1, 8, 1500), (1, 1, 9, 2000)])
+def test_every_new_element_not_finite_with_a_few_rows(H, K, n, length):
+    """The V rows of all new tokens but the first hold infinities in every channel: the lanes of a warp zero each other's
+    operands, and no row before a token may see 0 times its infinity."""
+    c = Case(H, K, [n, 1], [length, 33], seed=11)
+    new = torch.arange(length - n + 1, length, device=DEV)
+    c.v[c.ko[0] + new] = torch.where(torch.arange(128, device=DEV) % 2 == 0, torch.inf, -torch.inf).to(torch.bfloat16)
+    first = None
+    for _ in range(20):
+        c.out.fill_(9.0)
+        c.run()
+        assert c.out[0].isfinite().all()  # the first new row sees none of them
+        assert c.out[1:n, :, 0::2].eq(torch.inf).all() and c.out[1:n, :, 1::2].eq(-torch.inf).all()
+        first = c.out.clone() if first is None else first
+        assert torch.equal(c.out, first)
+    c.check()
