@@ -255,6 +255,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _bytes(workspace) -> int:
+    """Bytes that a call may write at a workspace's address: an expanded tensor has fewer than its elements take."""
+    if workspace is None or workspace.numel() == 0:
+        return 0
+    reach = 1 + sum((n - 1) * s for n, s in zip(workspace.shape, workspace.stride()))
+    return min(workspace.numel(), reach) * workspace.element_size()
+
+
 def lsa_version() -> int:
     return load_library().lsa_version()
 
@@ -301,7 +309,7 @@ def lsa_index(q_idx: torch.Tensor, k_idx: torch.Tensor, w: torch.Tensor, w_max: 
     lib = load_library()
     n_q, H_I, d_I = q_idx.shape
     cb = batch.c()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _bytes(workspace)
     st = lib.lsa_index(_ptr(q_idx), _ptr(k_idx), _ptr(w), w_max, H_I, d_I, ctypes.byref(cb), budget.c(),
                        _ptr(block_sums), 0 if block_sums is None else block_sums.shape[0], _ptr(index_sets),
                        _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
@@ -346,7 +354,7 @@ def lsa_append_index(k_idx_new: torch.Tensor, k_new: list, v_new: list, k: list,
     arr = ctypes.c_void_p * max(G, 1)
     kn, vn, kc, vc = (arr(*[t.data_ptr() for t in x]) for x in (k_new, v_new, k, v))
     cb = batch.c()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _bytes(workspace)
     rows = block_sums.shape[0] if block_sums is not None else 0
     st = lib.lsa_append_index(_ptr(k_idx_new), kn, vn, kc, vc, row_bytes, G, n_new, _ptr(q_idx), _ptr(k_idx), _ptr(w),
                               w_max, H_I, d_I, ctypes.byref(cb), budget.c(), _ptr(block_sums), rows,
@@ -371,7 +379,7 @@ def lsa_attend(q: list, k: list, v: list, index_sets: torch.Tensor, batch: Batch
     qa, ka, va, oa = (arr(*[t.data_ptr() for t in x]) for x in (q, k, v, out))
     cb = batch.c()
     st = lib.lsa_attend(qa, ka, va, H_q, H_kv, d, _ptr(index_sets), index_sets.shape[1], ctypes.byref(cb), G, oa,
-                        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                        _ptr(workspace), _bytes(workspace), _ptr(dev_status),
                         _stream(stream))
     _check("lsa_attend", st)
 
@@ -401,7 +409,7 @@ def lsa_attend_grouped(q: list, k: list, v: list, index_sets: torch.Tensor, batc
     qa, ka, va, oa = (arr(*[t.data_ptr() for t in x]) for x in (q, k, v, out))
     cb = batch.c()
     st = lib.lsa_attend_grouped(qa, ka, va, H_q, H_kv, d, _ptr(index_sets), index_sets.shape[1], ctypes.byref(cb),
-                                G, group_rows, oa, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                G, group_rows, oa, _ptr(workspace), _bytes(workspace),
                                 _ptr(dev_status), _stream(stream))
     _check("lsa_attend_grouped", st)
 
@@ -428,7 +436,7 @@ def lsa_attend_si(q: list, k: list, v: list, index_sets: torch.Tensor, budget: B
     qa, ka, va, oa = (arr(*[t.data_ptr() for t in x]) for x in (q, k, v, out))
     cb = batch.c()
     st = lib.lsa_attend_si(qa, ka, va, H_q, H_kv, d, _ptr(index_sets), budget.c(), ctypes.byref(cb), G, oa,
-                           _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                           _ptr(workspace), _bytes(workspace), _ptr(dev_status),
                            _stream(stream))
     _check("lsa_attend_si", st)
 
@@ -448,7 +456,7 @@ def lsa_attend_lse(q: list, k: list, v: list, index_sets: torch.Tensor, batch: B
     qa, ka, va, oa, la = (arr(*[t.data_ptr() for t in x]) for x in (q, k, v, out, lse))
     cb = batch.c()
     st = lib.lsa_attend_lse(qa, ka, va, H_q, H_kv, d, _ptr(index_sets), index_sets.shape[1], ctypes.byref(cb), G, oa,
-                            la, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                            la, _ptr(workspace), _bytes(workspace), _ptr(dev_status),
                             _stream(stream))
     _check("lsa_attend_lse", st)
 
@@ -501,7 +509,7 @@ def lsa_attend_fp8(q: list, k8: list, v8: list, k_scale: list, v_scale: list, in
     ks, vs = fa(*[float(x) for x in k_scale]), fa(*[float(x) for x in v_scale])
     cb = batch.c()
     st = lib.lsa_attend_fp8(qa, ka, va, ks, vs, H_q, H_kv, d, _ptr(index_sets), index_sets.shape[1],
-                            ctypes.byref(cb), G, oa, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                            ctypes.byref(cb), G, oa, _ptr(workspace), _bytes(workspace),
                             _ptr(dev_status), _stream(stream))
     _check("lsa_attend_fp8", st)
 

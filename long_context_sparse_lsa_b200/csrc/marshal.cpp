@@ -144,6 +144,8 @@ struct Lists {
         *bytes = 0;
         if (o == Py_None) return nullptr;
         const at::Tensor& t = note(tensor(name, o));
+        // (an expanded tensor has fewer bytes behind its address than elements)
+        if (!t.is_contiguous()) type_error(std::string(name) + " must be a contiguous tensor");
         *bytes = (size_t)t.nbytes();
         return t.data_ptr();
     }

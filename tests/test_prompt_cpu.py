@@ -59,3 +59,28 @@ def test_binding_refuses_wrong_tensors():
                     (dict(dev_status=t(bf, 1)), TypeError), (dict(), ValueError)]:  # (the last: host tensors)
         with pytest.raises(err):
             lsa.lsa_attend_prompt(**{**ok, **kw}, stream=0)
+
+
+def test_binding_refuses_an_expanded_workspace():
+    """Its elements are more than the bytes behind its address."""
+    t = lambda dtype, *s: torch.zeros(s, dtype=dtype)
+    bf, u8 = torch.bfloat16, torch.uint8
+    wide = t(u8, 1).expand(1 << 30)
+    pr = lsa.Prompts(t(torch.int32, 2), t(torch.int64, 1), t(torch.int32, 1), 3, 10, 10)
+    b = lsa.Batch(t(torch.int64, 1), t(torch.int32, 1), t(torch.int32, 3), t(torch.int32, 3), 10, 10)
+    q, kv, sets, out = t(bf, 3, 8, 128), t(bf, 10, 2, 128), t(torch.int32, 3, 1024), t(torch.float32, 3, 8, 128)
+    for ws in (wide, t(u8, 4096)[::2]):
+        with pytest.raises(TypeError, match="workspace"):
+            lsa.lsa_attend_prompt(q, kv, kv, pr, torch.empty_like(q), ws, stream=0)
+        with pytest.raises(TypeError, match="workspace"):
+            lsa.lsa_attend_fp4([q], [t(u8, 10, 2, 64)], [t(u8, 10, 2, 8)], [t(u8, 10, 2, 64)], [t(u8, 10, 2, 8)], [1.0], [1.0],
+                               sets, b, [out], ws, stream=0)
+    # the calls that take any tensor count what lies behind the address (refused before any launch)
+    assert lsa._bytes(wide) == 1 and lsa._bytes(t(torch.float32, 6, 2).T) == 48 and lsa._bytes(t(u8, 0)) == 0
+    assert lsa._bytes(None) == 0 and lsa._bytes(t(u8, 8)[::2]) == 4
+    need = lsa.lsa_attend_workspace_size(b, 8, 2, 128, 1024, 1)
+    assert need > 1
+    for ws in (t(u8, 1).expand(need), None):
+        with pytest.raises(lsa.LsaError) as e:
+            lsa.lsa_attend([q], [kv], [kv], sets, b, [out], ws, stream=0)
+        assert e.value.status == WORKSPACE
