@@ -224,8 +224,9 @@ __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int b) {
 }
 
 // Item i (every lane of the warp calls it). Sequences' tiles come longest first.
-__device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool report) {
+__device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i) {
     PrItem it;
+    if (i == 0 && lane_id() == 0 && rows_outside(a.row_offset, a.n_seq, a.n_rows)) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
     it.split = i % a.n_splits;
     it.kvh = i / a.n_splits % a.H_kv;
     const int slot = i / a.n_splits / a.H_kv;
@@ -236,7 +237,7 @@ __device__ __forceinline__ PrItem pr_item(const PromptArgs& a, int i, bool repor
     const int tiles = (it.sq.n + tc - 1) / tc;
     it.live = it.sq.n > 0 && local >= 0 && local < tiles ? 1 : 0;
     if (it.live && !it.sq.ok) {
-        if (report && local == 0 && lane_id() == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
+        if (local == 0 && lane_id() == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
         it.live = 0;
     }
     if (!it.live) return it;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
                 ++handed;
             };
             for (int i = (int)blockIdx.x; ok && i >= 0;) {
-                const PrItem it = pr_item(a, i, true);
+                const PrItem it = pr_item(a, i);
                 if (it.live) hand_out(it);
                 // The item after this one is asked for with this one's last two key tiles: a
                 // CTA that asks at an item's start takes items that idle ones could start on

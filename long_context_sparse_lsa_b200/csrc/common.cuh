@@ -204,6 +204,12 @@ __device__ __forceinline__ int find_last(int n, Le le) {
     return lo;
 }
 
+// Whether some sequence has rows outside [0, n_rows) (offsets ascend): a kernel
+// that goes by rows, or by tiles of them, may never come to such a sequence.
+__device__ __forceinline__ bool rows_outside(const int32_t* row_offset, int n_seq, int n_rows) {
+    return row_offset[0] < 0 || row_offset[n_seq] > n_rows;
+}
+
 // Pairs of floats in one register pair: one instruction for both.
 using f32x2 = uint64_t;
 __device__ __forceinline__ f32x2 pair(float lo, float hi) {

@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
             s_dst[i] = dst;
         }
     }
+    if (blockIdx.x + blockIdx.y == 0 && tid == kWarp && rows_outside(a.row_offset, a.n_seq, a.n_rows))
+        flag(a.dev_status, LSA_DEV_BAD_LENGTH);
     const float S = is_v ? a.v_scale[layer] : a.k_scale[layer];
     __syncthreads();
 #pragma unroll

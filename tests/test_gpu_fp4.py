@@ -426,3 +426,22 @@ def test_store_many_rows(H, G, rows, lens):
             assert np.array_equal(group[g].cpu().numpy(), full_g) and np.array_equal(code[g].cpu().numpy(), full_c)
             assert torch.equal(code[g], code2[g]) and torch.equal(group[g], group2[g])
             assert torch.equal(rnd[g].cpu(), torch.tensor(wv).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("ro,here", [([0, 2, 7, 9], (0, 1)), ([0, 2, 7, 5000], (0, 1)), ([0, 2, 100000, 100003], (0,)),
+                                     ([-3, 0, 4, 7], (1, 2)), ([-4000, -3995, 0, 7], (2,)), ([7, 9, 10, 12], ())])
+def test_store_flags_sequences_outside_the_rows(ro, here):
+    """Also one none of whose rows lies in the buffers."""
+    n_rows, lens, ko = 7, [8, 8, 8], [0, 8, 16]
+    x = _rand((n_rows, 2, 128), 3)
+    k, kg, v, vg = _caches(24, 2, 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lsa.lsa_store_fp4([x], [x], k, kg, v, vg, [1.0], [1.0], lsa.Prompts(_i32(ro), _i64(ko), _i32(lens), n_rows, 8, 24),
+                      dev_status=status)
+    assert status.item() == lsa.LSA_DEV_BAD_LENGTH
+    want = np.full((24, 2, 64), 0xA5, np.uint8)
+    codes = fp4.quantise(x, 1.0)[0]
+    for b in here:
+        n = ro[b + 1] - ro[b]
+        want[ko[b] + lens[b] - n:ko[b] + lens[b]] = codes[ro[b]:ro[b + 1]]
+    assert np.array_equal(k[0].cpu().numpy(), want) and np.array_equal(v[0].cpu().numpy(), want)

@@ -366,3 +366,35 @@ def test_every_new_element_not_finite_with_a_few_rows(H, K, n, length):
         first = c.out.clone() if first is None else first
         assert torch.equal(c.out, first)
     c.check()
+
+
+@pytest.mark.parametrize("where", ["behind", "far behind", "before", "far before"])
+@pytest.mark.parametrize("rows", [[20, 30, 40, 9], [1, 2, 1, 1], [300, 0, 100, 2000]])
+def test_sequences_that_lie_outside_the_rows(where, rows):
+    """A sequence none of whose rows lies in the buffers is flagged like one that passes their end."""
+    c = Case(8, 1, rows, [max(n, 50) for n in rows], seed=12)
+    out = 3 if "behind" in where else 0
+    far = 1 << 20 if "far" in where else 0
+    if out == 3:  # the last sequence starts at the end of the rows, or far behind
+        c.n -= rows[3]
+        c.pr.row_offset[3 if far else 4] += far
+        c.pr.row_offset[4] += far if far else 0
+    else:  # the first one lies before them
+        c.n -= rows[0]
+        c.ro = [x - rows[0] for x in c.ro]
+        c.pr.row_offset -= rows[0]
+        c.pr.row_offset[0] -= far
+        c.pr.seq_lens[0] += far
+        c.pr.max_len += far
+    lo = 0 if out == 3 else rows[0]
+    c.q, c.out, c.lse = (x[lo:lo + c.n].contiguous() for x in (c.q, c.out, c.lse))
+    c.pr.n_rows = c.n
+    c.ws = torch.empty(max(256, lsa.lsa_attend_prompt_workspace_size(c.pr, 8, 1, 128)), dtype=torch.uint8, device=DEV)
+    c.run()
+    assert c.status.item() == lsa.LSA_DEV_BAD_LENGTH
+    c.status.zero_()
+    skip = [out] + ([2] if out == 3 and far else [])  # (far behind, the sequence before passes the end of the rows)
+    c.check(skip=skip)
+    for b in skip:
+        if b != out:
+            assert (c.out[c.ro[b]:c.ro[b + 1]] == 9).all()
