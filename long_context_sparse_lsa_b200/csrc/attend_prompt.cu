@@ -781,14 +781,15 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     // CTAs as run at once (two an SM), but four parts of the longest sequence
     // at least (so that long and short ones even out), 128 at most, and 128
     // keys a part. 16 single tokens over up to 3136 tokens, 32/4 heads: 16 us
-    // there, 31 us here; 64 over up to 8000: 89 and 201 us.
+    // there, 31 us here; 64 over up to 8000: 89 and 201 us. That is the mean: a
+    // sequence of more columns gets further CTAs there, which take turns.
     // Up to eight parts are joined in a cluster where all clusters run at once (16
     // tokens over up to 500: 6.5 us, with the merge kernel 7.9; where they do not,
     // finished CTAs wait in the way of others: 64 tokens over up to 500 22.5 and
     // 16.7 us; 9 over up to 1000, eight parts on 97% of the places, 9.8 and 8.2),
     // and parts of up to 256 keys are taken for that (4 over up to 2000: 7.0
     // against 8.6 us).
-    p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65535;
+    p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65000;
     if (p.few) {
         const int64_t units = (int64_t)n_seq * H_kv;
         int64_t parts = (2 * (int64_t)num_sms + units - 1) / units;
@@ -798,6 +799,10 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
         p.part_keys = (int)((((int64_t)max_len + parts - 1) / parts + 63) / 64 * 64);
         if (p.part_keys < 128) p.part_keys = 128;
         p.n_parts = (int)(((int64_t)max_len + p.part_keys - 1) / p.part_keys);
+        // further runs of columns: all there could be (if one sequence had all rows), or as many as run at once
+        const int64_t runs = ((int64_t)n_rows * p.G - 1) / few_columns(n_seq, n_rows, p.G);
+        const int64_t at_a_time = 2 * num_sms / ((int64_t)p.n_parts * H_kv);
+        p.helpers = (int)(runs < at_a_time || runs == 0 ? runs : at_a_time > 1 ? at_a_time : 1);
         if (p.n_parts > kFewJoined || !at_once(p.n_parts)) workspace();
         return p;
     }

@@ -19,6 +19,15 @@
 // part has a fixed number of keys, so that CTAs are alike whatever the
 // sequences' lengths; those behind a sequence's end have nothing to do. In a
 // cluster it is an equal share of its sequence.
+//  * Whether a batch comes here goes by its mean of rows, so single sequences
+// may have many more columns than the 8 or 16 that a CTA takes. Such further
+// runs of columns are other CTAs' work: about as many as run at once, behind
+// the sequences' own in the grid, take them in turn (one chunk of 64 rows on
+// 65536 tokens beside 63 single tokens on up to 3136, 32/4 heads: 7604 us with
+// all runs one after the other in the sequence's own CTAs, 516 so, and 879 on
+// the 128-row tiles of attend_prompt.cu; one of 17 beside 15, on up to 3136: 97,
+// 28 and 30; one of 64 on 16384 tokens in 64 slots, the others empty: 2853, 204
+// and 214). With nothing to take they cost less than the calls' spread.
 #include "common.cuh"
 #include "internal.h"
 #include "prompt_parts.cuh"
@@ -46,6 +55,52 @@ __device__ __forceinline__ float ex2(float x) {
 // 16-byte chunk c of row m, so that eight rows' equal chunks fall on all banks.
 __device__ __forceinline__ uint32_t fw_at(int m, int c) { return (uint32_t)(m * kFwRow + 16 * (c ^ (m & 7))); }
 
+// The i-th of all sequences' runs of W columns behind each one's first: its
+// sequence and first column; false behind the last. A warp looks at 32 kEach
+// sequences a step, a lane at every 32nd of them (and counts its own in a row).
+template <int W, int kEach>
+__device__ __forceinline__ bool find_columns(const PromptArgs& a, int i, int& seq, int& c0) {
+    const int lane = lane_id();
+    auto runs = [&](int b) {
+        const int n = min(a.row_offset[min(b + 1, a.n_seq)] - a.row_offset[min(b, a.n_seq)], a.n_rows);
+        return n > 0 ? (n * a.G - 1) / W : 0;
+    };
+    for (int b0 = 0; b0 < a.n_seq; b0 += kEach * kWarp) {
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) mine += runs(b0 + kWarp * j + lane);
+        if (!__any_sync(0xffffffffu, mine > 0)) continue;
+        int upto = mine;
+#pragma unroll
+        for (int k = 1; k < kWarp; k <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, k);
+            if (lane >= k) upto += x;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, upto > i);
+        if (here == 0u) {
+            i -= __shfl_sync(0xffffffffu, upto, kWarp - 1);
+            continue;
+        }
+        const int owner = __ffs(here) - 1;
+        i -= __shfl_sync(0xffffffffu, upto - mine, owner);
+        seq = b0 + owner;
+        for (int r = runs(seq); i >= r; r = runs(seq)) {  // (the owner has more than i)
+            i -= r;
+            seq += kWarp;
+        }
+        c0 = (i + 1) * W;
+        return true;
+    }
+    return false;
+}
+// Few steps where there are many sequences, few loads a step where there are
+// not (nothing found: 60000 sequences of 3 tokens 592 us with 32 a lane, 643
+// with 8; 16 over up to 500 tokens 7.0 and 6.2).
+template <int W>
+__device__ __forceinline__ bool further_columns(const PromptArgs& a, int i, int& seq, int& c0) {
+    return a.n_seq > 8192 ? find_columns<W, 32>(a, i, seq, c0) : find_columns<W, 8>(a, i, seq, c0);
+}
+
 // NT: tiles of 8 (row, query head) columns taken at a time. JOINED: the parts
 // of a sequence are a cluster.
 template <int NT, bool JOINED>
@@ -53,45 +108,56 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = lane_id(), warp = warp_id();
     const int g = lane >> 2, t4 = lane & 3;
-    const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
-    const int row0 = a.row_offset[seq], n = a.row_offset[seq + 1] - row0;
-    const int len = a.seq_lens[seq];
-    const int64_t off = a.kv_offset[seq];
-    pdl_enter();
-    if (n <= 0) return;
-    if (row0 < 0 || (int64_t)row0 + n > a.n_rows || n > len || len > a.max_len || off < 0 || off + len > a.total_tokens) {
-        if (tid == 0 && part == 0 && kvh == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
-        return;
-    }
-    const int base = len - n;                     // tokens before the first row
-    // (a cluster's parts are equal shares of the sequence)
-    const int part_keys = JOINED ? ((len + a.n_parts - 1) / a.n_parts + kFwTile - 1) / kFwTile * kFwTile : a.part_keys;
-    const int k_lo = min(len, part * part_keys), k_hi = min(len, k_lo + part_keys);
-    if (!JOINED && k_lo >= len) return;
-    const int n_tiles = max(0, k_hi - k_lo + kFwTile - 1) / kFwTile;
-    const int G = a.G, cols = n * G;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFwRing * kFwTileBytes);
-    const uint16_t* kb = a.k + off * a.k_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
-    const uint16_t* vb = a.v + off * a.v_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
-    // a lane copies 16-byte chunk lane % 16 of rows lane / 16, + 2, ...; rows behind the part are zeros
-    auto fetch = [&](int i, int slot) {
-        if (i < n_tiles) {
-            const uint32_t to = ring + (uint32_t)(slot * kFwTileBytes);
-#pragma unroll
-            for (int x = 0; x < kFwTile / 2; ++x) {
-                const int m = 2 * x + (lane >> 4);
-                const int key = k_lo + i * kFwTile + m;
-                const uint32_t nb = key < k_hi ? 16u : 0u;
-                const int64_t at = min(key, k_hi - 1);
-                cp_async16(to + fw_at(m, lane & 15), kb + at * a.k_stride, nb);
-                cp_async16(to + (uint32_t)(kFwTile * kFwRow) + fw_at(m, lane & 15), vb + at * a.v_stride, nb);
-            }
-        }
-        cp_async_commit();
+    const int part = blockIdx.x, kvh = blockIdx.y;
+    const int helper = (int)blockIdx.z - a.n_seq;  // behind the sequences' CTAs: those for further columns
+    int seq = blockIdx.z, c0 = 0, row0 = 0, n = 0, len = 0;
+    int64_t off = 0;
+    auto look_up = [&]() {
+        row0 = a.row_offset[seq];
+        n = a.row_offset[seq + 1] - row0;
+        len = a.seq_lens[seq];
+        off = a.kv_offset[seq];
     };
+    bool found = helper < 0 || further_columns<8 * NT>(a, helper, seq, c0);
+    if (found) look_up();
+    pdl_enter();
+    for (int turn = helper; found; found = helper >= 0 && further_columns<8 * NT>(a, turn += a.helpers, seq, c0)) {
+        if (turn != helper) {
+            __syncthreads();  // the merge area of the columns before
+            look_up();
+        }
+        if (n <= 0) continue;
+        if (row0 < 0 || (int64_t)row0 + n > a.n_rows || n > len || len > a.max_len || off < 0 || off + len > a.total_tokens) {
+            if (tid == 0 && part == 0 && kvh == 0 && c0 == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
+            continue;
+        }
+        const int base = len - n;                     // tokens before the first row
+        // (a cluster's parts are equal shares of the sequence)
+        const int part_keys = JOINED ? ((len + a.n_parts - 1) / a.n_parts + kFwTile - 1) / kFwTile * kFwTile : a.part_keys;
+        const int k_lo = min(len, part * part_keys), k_hi = min(len, k_lo + part_keys);
+        if (!JOINED && k_lo >= len) continue;
+        const int n_tiles = max(0, k_hi - k_lo + kFwTile - 1) / kFwTile;
+        const int G = a.G, cols = n * G;
+        const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFwRing * kFwTileBytes);
+        const uint16_t* kb = a.k + off * a.k_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
+        const uint16_t* vb = a.v + off * a.v_stride + (int64_t)kvh * kFwD + 8 * (lane & 15);
+        // a lane copies 16-byte chunk lane % 16 of rows lane / 16, + 2, ...; rows behind the part are zeros
+        auto fetch = [&](int i, int slot) {
+            if (i < n_tiles) {
+                const uint32_t to = ring + (uint32_t)(slot * kFwTileBytes);
+    #pragma unroll
+                for (int x = 0; x < kFwTile / 2; ++x) {
+                    const int m = 2 * x + (lane >> 4);
+                    const int key = k_lo + i * kFwTile + m;
+                    const uint32_t nb = key < k_hi ? 16u : 0u;
+                    const int64_t at = min(key, k_hi - 1);
+                    cp_async16(to + fw_at(m, lane & 15), kb + at * a.k_stride, nb);
+                    cp_async16(to + (uint32_t)(kFwTile * kFwRow) + fw_at(m, lane & 15), vb + at * a.v_stride, nb);
+                }
+            }
+            cp_async_commit();
+        };
 
-    for (int c0 = 0; c0 < cols; c0 += 8 * NT) {
-        if (c0 > 0) __syncthreads();  // the merge area of the columns before
         float* join = reinterpret_cast<float*>(smem + fw_join_at(NT));  // [column][kFwJoinRow], then [column] (m, l)
         float2* join_ml = reinterpret_cast<float2*>(join + 8 * NT * kFwJoinRow);
 #pragma unroll
@@ -253,7 +319,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
                 x[(34 + c) * kWarp] = l_run[t][c];
             }
         }
-        if (c0 + 8 * NT >= cols) pdl_trigger();
+        if (helper < 0) pdl_trigger();
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -346,15 +412,14 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
 
 cudaError_t launch_attend_prompt_few(const PromptArgs& a, int parts, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed[4];
-    // columns of most sequences: 8 or fewer (one token of up to 8 heads), or more
-    const bool wide = (int64_t)a.n_rows * a.G > (int64_t)a.n_seq * 8;
+    const bool wide = few_columns(a.n_seq, a.n_rows, a.G) > 8;
     const bool joined = parts > 1 && a.part_o == nullptr;
     auto kern = wide ? (joined ? attend_prompt_few_kernel<2, true> : attend_prompt_few_kernel<2, false>)
                      : (joined ? attend_prompt_few_kernel<1, true> : attend_prompt_few_kernel<1, false>);
     const cudaError_t e = allow_smem(kern, kFwSmem, allowed[wide + 2 * joined]);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)parts, (unsigned)a.H_kv, (unsigned)a.n_seq), dim3(kFwThreads), kFwSmem, stream,
-                      joined ? parts : 0, a);
+    return launch_pdl(kern, dim3((unsigned)parts, (unsigned)a.H_kv, (unsigned)(a.n_seq + a.helpers)), dim3(kFwThreads), kFwSmem,
+                      stream, joined ? parts : 0, a);
 }
 
 }  // namespace lsa

@@ -398,3 +398,38 @@ def test_sequences_that_lie_outside_the_rows(where, rows):
     for b in skip:
         if b != out:
             assert (c.out[c.ro[b]:c.ro[b + 1]] == 9).all()
+
+
+@pytest.mark.parametrize("H,K", [(8, 1), (32, 4), (2, 2), (6, 2)])
+@pytest.mark.parametrize("many,long", [(3, [3]), (15, [17]), (63, [40, 2, 25]), (700, [256, 5, 300]), (9000, [129, 400, 7])])
+def test_chunks_among_single_tokens(H, K, many, long):
+    """Single tokens, and a few sequences with many more (row, head) columns than the mean that chooses the kernel."""
+    rows = [1] * many
+    for i, n in enumerate(long):  # somewhere, and the last at the end
+        rows.insert(len(rows) if i + 1 == len(long) else (i + 1) * many // 3, n)
+    big = [i for i, n in enumerate(rows) if n > 1]
+    lens = [max(n, 1 + (37 * i) % (300 if many < 500 else 20)) for i, n in enumerate(rows)]
+    for i in big:
+        lens[i] = rows[i] + 500
+    c = Case(H, K, rows, lens, seed=many, gap=1).run()
+    c.check(skip=() if many < 100 else set(range(len(rows))) - set(big) - set(range(0, len(rows), many // 25)))
+
+
+def test_a_chunk_in_one_of_many_slots_takes_no_pass_after_pass():
+    """64 slots, 63 of them empty, one of 64 rows on 16384 tokens, against the same chunk alone: the mean chooses the kernel
+    for a few rows, whose passes over K and V for 16 columns each must not follow one another on a few CTAs (93 times the
+    chunk alone, and 7 times now)."""
+    def ms(c):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        times = []
+        for _ in range(8):
+            ev[0].record()
+            c.run()
+            ev[1].record()
+            torch.cuda.synchronize()
+            times.append(ev[0].elapsed_time(ev[1]))
+        return sorted(times)[3]
+
+    slots, alone = Case(32, 4, [64] + [0] * 63, [16384] + [1] * 63), Case(32, 4, [64], [16384])
+    assert ms(slots) < 25 * ms(alone)
+    slots.check()
