@@ -146,9 +146,8 @@ def load_library():
     global _lib
     if _lib is not None:
         return _lib
-    for path in (LIB_PATH, _MARSHAL_PATH):
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m long_context_sparse_lsa_b200.build`")
+    if not os.path.exists(LIB_PATH):
+        raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m long_context_sparse_lsa_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     lib.lsa_version.restype = i32
@@ -233,11 +232,28 @@ def load_library():
     lib.lsa_attend_noalloc.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i32, i32, vp,
                                        i32, ctypes.POINTER(_Batch), i32, ctypes.POINTER(vp), vp, vp]
     # the calls whose arguments _marshal (csrc/marshal.cpp) checks and hands over
-    lib.marshal = importlib.import_module("._marshal", __package__)
     for name in ("store_fp4", "attend_fp4", "attend_prompt"):
         setattr(lib, name + "_at", ctypes.cast(getattr(lib, "lsa_" + name), vp).value)
     _lib = lib
     return lib
+
+
+_marshal = None
+
+
+def _marshalling():
+    """The compiled argument handling, loaded by the first call that goes through it: it is bound to the Python and torch
+    of its build, the library is not."""
+    global _marshal
+    if _marshal is None:
+        how = "build it with `python -m long_context_sparse_lsa_b200.build`"
+        if not os.path.exists(_MARSHAL_PATH):
+            raise RuntimeError(f"{_MARSHAL_PATH} is missing: {how}")
+        try:
+            _marshal = importlib.import_module("._marshal", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"{_MARSHAL_PATH} does not fit this Python and torch: {how}") from e
+    return _marshal
 
 
 def _check(func: str, status: int):
@@ -539,9 +555,9 @@ def lsa_store_fp4(k_new: list, v_new: list, k: list, k_group: list, v: list, v_g
     [T, H_kv, 8]) with per-layer power-of-two scales. k_round, v_round: the values the caches now hold (bf16
     [n_rows, H_kv, 128])."""
     lib, p = load_library(), prompts
-    st = lib.marshal.store_fp4(lib.store_fp4_at, k_new, v_new, k, k_group, v, v_group, k_scale, v_scale, p.row_offset,
-                               p.kv_offset, p.seq_lens, p.n_rows, p.max_len, p.total_tokens, k_round, v_round, dev_status,
-                               stream)
+    st = _marshalling().store_fp4(lib.store_fp4_at, k_new, v_new, k, k_group, v, v_group, k_scale, v_scale, p.row_offset,
+                                  p.kv_offset, p.seq_lens, p.n_rows, p.max_len, p.total_tokens, k_round, v_round,
+                                  dev_status, stream)
     if st:
         _check("lsa_store_fp4", st)
 
@@ -561,8 +577,9 @@ def lsa_attend_fp4(q: list, k: list, k_group: list, v: list, v_group: list, k_sc
     """lsa_attend over 4-bit K/V caches: codes uint8 [T, H_kv, 64], group scales uint8 E4M3 [T, H_kv, 8], per-layer
     scales (lists of G tensors and floats)."""
     lib, b = load_library(), batch
-    st = lib.marshal.attend_fp4(lib.attend_fp4_at, q, k, k_group, v, v_group, k_scale, v_scale, index_sets, b.kv_offset,
-                                b.seq_lens, b.q_seq, b.q_len, b.max_len, b.total_tokens, out, workspace, dev_status, stream)
+    st = _marshalling().attend_fp4(lib.attend_fp4_at, q, k, k_group, v, v_group, k_scale, v_scale, index_sets, b.kv_offset,
+                                   b.seq_lens, b.q_seq, b.q_len, b.max_len, b.total_tokens, out, workspace, dev_status,
+                                   stream)
     if st:
         _check("lsa_attend_fp4", st)
 
@@ -583,8 +600,8 @@ def lsa_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, prompts
     [T, H_kv, 128] (views whose rows are apart, as of a fused projection, are taken as they are), out bf16 [n_rows,
     H_q, 128], lse fp32 [n_rows, H_q] or None."""
     lib, p = load_library(), prompts
-    st = lib.marshal.attend_prompt(lib.attend_prompt_at, q, k, v, p.row_offset, p.kv_offset, p.seq_lens, p.n_rows, p.max_len,
-                                   p.total_tokens, out, workspace, lse, dev_status, stream)
+    st = _marshalling().attend_prompt(lib.attend_prompt_at, q, k, v, p.row_offset, p.kv_offset, p.seq_lens, p.n_rows,
+                                      p.max_len, p.total_tokens, out, workspace, lse, dev_status, stream)
     if st:
         _check("lsa_attend_prompt", st)
 

@@ -64,14 +64,16 @@ def _build_marshal(nvcc: str, verbose: bool) -> None:
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
            sysconfig.get_paths()["include"], INCLUDE]
     tmp = MARSHAL + ".tmp"
-    cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = [nvcc, "-O2", "-shared", "-std=c++17", "-cudart", "none", "-Xcompiler", "-fPIC",  # (nvcc's host compiler)
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *["-I" + d for d in inc], os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(base, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for marshal.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError("marshal.cpp, which the 4-bit and whole-prompt calls need, did not build (the library did):\n"
+                           f"{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
 
 
@@ -97,7 +99,6 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         marshal = ex.submit(_build_marshal, nvcc, verbose)
         objs = list(ex.map(compile_one, sources()))
-        marshal.result()
     tmp = LIBRARY + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     if verbose:
@@ -106,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
+    marshal.result()  # the library stands, and its other calls, where this one fails
     return LIBRARY
 
 
