@@ -15,6 +15,8 @@ from dataclasses import dataclass
 
 import torch
 
+from .build import built_for
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblsa.so")
 _MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
@@ -250,9 +252,12 @@ def _marshalling():
         if not os.path.exists(_MARSHAL_PATH):
             raise RuntimeError(f"{_MARSHAL_PATH} is missing: {how}")
         try:
-            _marshal = importlib.import_module("._marshal", __package__)
+            module = importlib.import_module("._marshal", __package__)
         except ImportError as e:
             raise RuntimeError(f"{_MARSHAL_PATH} does not fit this Python and torch: {how}") from e
+        if module.built_for != built_for():  # (it may load, and read tensors by another layout)
+            raise RuntimeError(f"{_MARSHAL_PATH} is built for {module.built_for}, not for {built_for()}: {how}")
+        _marshal = module
     return _marshal
 
 

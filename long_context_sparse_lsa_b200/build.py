@@ -52,7 +52,17 @@ def up_to_date() -> bool:
     if not (os.path.exists(LIBRARY) and os.path.exists(MARSHAL)):
         return False
     t = min(os.path.getmtime(LIBRARY), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _deps() + [os.path.abspath(__file__)])
+    if any(os.path.getmtime(f) > t for f in _deps() + [os.path.abspath(__file__)]):
+        return False
+    with open(MARSHAL, "rb") as f:
+        return built_for().encode() + b"\0" in f.read()
+
+
+def built_for() -> str:
+    """What _marshal.so is compiled against. It holds this text; another Python or torch cannot use it."""
+    import torch
+
+    return f"{sysconfig.get_config_var('SOABI')}, torch {torch.__version__}"
 
 
 def _build_marshal(nvcc: str, verbose: bool) -> None:
@@ -62,7 +72,9 @@ def _build_marshal(nvcc: str, verbose: bool) -> None:
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
-           sysconfig.get_paths()["include"], INCLUDE]
+           sysconfig.get_paths()["include"], INCLUDE, BUILD_DIR]
+    with open(os.path.join(BUILD_DIR, "built_for.h"), "w") as f:
+        f.write(f'#define LSA_BUILT_FOR "{built_for()}"\n')
     tmp = MARSHAL + ".tmp"
     cmd = [nvcc, "-O2", "-shared", "-std=c++17", "-cudart", "none", "-Xcompiler", "-fPIC",  # (nvcc's host compiler)
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

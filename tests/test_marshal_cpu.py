@@ -66,3 +66,24 @@ def test_the_library_stands_where_the_module_does_not_build(compilers):
         build.build(force=True)
     assert os.path.exists(build.LIBRARY) and not os.path.exists(build.MARSHAL)
     assert {c[0] for c in calls} == {"/usr/local/cuda/bin/nvcc"}  # no compiler but nvcc (and its own host compiler)
+
+
+def test_a_module_of_another_build_is_not_used(monkeypatch):
+    monkeypatch.setattr(lsa, "_marshal", None)
+    assert lsa._marshalling().built_for == build.built_for()
+    monkeypatch.setattr(lsa, "_marshal", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="torch 1.0.0"):
+        _prompt_call()
+
+
+def test_a_module_of_another_build_is_not_up_to_date(compilers, monkeypatch):
+    build.build(force=True)
+    with open(build.MARSHAL, "w") as f:
+        f.write(f"...{build.built_for()}\0...")
+    assert build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "0")
+    assert not build.up_to_date()
+    build.build()
+    with open(os.path.join(build.BUILD_DIR, "built_for.h")) as f:
+        assert f'"{build.built_for()}"' in f.read()
