@@ -769,7 +769,7 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     PromptPlan p;
     p.G = H_q / H_kv;
     p.tile_tokens = kPrRows / p.G;
-    const int key_tiles = (max_len + kPrKeys - 1) / kPrKeys;
+    const int key_tiles = (int)(((int64_t)max_len + kPrKeys - 1) / kPrKeys);
     auto workspace = [&]() {
         if (p.n_parts == 1) return;
         const size_t rows = (size_t)p.n_parts * n_rows * H_q;

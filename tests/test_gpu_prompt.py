@@ -433,3 +433,8 @@ def test_a_chunk_in_one_of_many_slots_takes_no_pass_after_pass():
     slots, alone = Case(32, 4, [64] + [0] * 63, [16384] + [1] * 63), Case(32, 4, [64], [16384])
     assert ms(slots) < 25 * ms(alone)
     slots.check()
+
+
+@pytest.mark.parametrize("rows,lens", [([100], [700]), ([40, 300], [40, 300]), ([1, 1], [5, 900]), ([1] * 200, [30 + i for i in range(200)])])
+def test_no_bound_on_the_lengths(rows, lens):
+    Case(8, 1, rows, lens, seed=2, max_len=2 ** 31 - 1).run().check()

@@ -84,3 +84,12 @@ def test_binding_refuses_an_expanded_workspace():
         with pytest.raises(lsa.LsaError) as e:
             lsa.lsa_attend([q], [kv], [kv], sets, b, [out], ws, stream=0)
         assert e.value.status == WORKSPACE
+
+
+@pytest.mark.parametrize("n_seq,n_rows,H,K", [(1, 100, 32, 4), (1, 1, 32, 4), (3, 700, 8, 8), (200, 200, 16, 1)])
+def test_the_plan_takes_any_bound_on_the_lengths(n_seq, n_rows, H, K):
+    """The largest max_len, as a caller without a bound gives it, is planned like one a little below."""
+    lib = lsa.load_library()
+    plans = [(lib.lsa_attend_prompt_workspace_size(p, H, K, 128), lib.lsa_attend_prompt_launches(p, H, K, 128))
+             for p in (_prompts(n_seq=n_seq, n_rows=n_rows, max_len=m) for m in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 300))]
+    assert plans[0] == plans[1] == plans[2] and plans[0][1] == 2
