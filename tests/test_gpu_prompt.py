@@ -438,3 +438,27 @@ def test_a_chunk_in_one_of_many_slots_takes_no_pass_after_pass():
 @pytest.mark.parametrize("rows,lens", [([100], [700]), ([40, 300], [40, 300]), ([1, 1], [5, 900]), ([1] * 200, [30 + i for i in range(200)])])
 def test_no_bound_on_the_lengths(rows, lens):
     Case(8, 1, rows, lens, seed=2, max_len=2 ** 31 - 1).run().check()
+
+
+@pytest.mark.parametrize("rows,lens", [([700, 40], [700, 900]), ([1, 2], [3000, 900]), ([1, 1], [500, 300]), ([100], [5000]), ([64] * 3, [2000, 64, 900])])
+@pytest.mark.parametrize("rising", [False, True])
+def test_log_sum_exp_of_large_scores(rows, lens, rising):
+    """Scores of hundreds, of random order or rising with the position (the running maximum moves in every tile).
+
+    Tolerance. A log-sum-exp moves by no more than its scores do. A score is a sum of 128 exact products, 16 an instruction:
+    each of the 8 instructions aligns 17 terms to the largest and drops what lies below 2^-23 of it, and no term or partial
+    sum exceeds S = sum |q_i k_i| / sqrt(d): 8 * 17 * 2^-23 S < 2^-15 S (largest S of the row's keys). Taking z c - m c,
+    m c + log2 l and the factor ln 2 rounds numbers of at most |lse|'s or S's size four times: 4 * 2^-23 S. LSE for the sum."""
+    c = Case(8, 1, rows, lens, scale=30.0, seed=14)
+    if rising:
+        for o, length in zip(c.ko, c.lens):
+            c.k[o:o + length] *= torch.linspace(0.1, 3, length, device=DEV).to(torch.bfloat16)[:, None, None]
+    c.run()
+    assert c.status.item() == 0
+    for b, n in enumerate(rows):
+        lse = c.want(b)[1]
+        k = c.k[c.ko[b]:c.ko[b] + lens[b]].double().abs().amax(0)  # of each channel
+        S = torch.einsum("rhd,kd->rh", c.q[c.ro[b]:c.ro[b] + n].double().abs(), k) / 128 ** 0.5
+        got = c.lse[c.ro[b]:c.ro[b] + n].double()
+        assert float(lse.abs().max()) > 80  # (the case is what it says)
+        assert ((got - lse).abs() <= LSE + (2.0 ** -15 + 2.0 ** -21) * S).all(), (b, float(((got - lse).abs() / S).max()))
