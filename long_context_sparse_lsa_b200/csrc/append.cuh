@@ -20,11 +20,11 @@ __device__ __forceinline__ int sbyte(uint32_t w, int i) { return static_cast<int
 __device__ __forceinline__ bool seq_ok(const BlockSumArgs& a, int seq, int64_t& off, int& len, bool report) {
     off = a.kv_offset[seq];
     len = a.seq_lens[seq];
-    bool ok = len >= 1 && len <= a.max_len && off >= 0 && off + len <= a.total_tokens;
+    bool ok = len >= 1 && len <= a.max_len && off >= 0 && off <= a.total_tokens - len;
     if (ok && a.hi_block > 0) {
         const int64_t boff = a.blk_offset[seq];
         const int nblk = (len + a.hi_block - 1) / a.hi_block;
-        ok = boff >= 0 && boff + nblk <= a.block_rows;
+        ok = boff >= 0 && boff <= a.block_rows - nblk;
     }
     if (!ok && report && threadIdx.x == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
     return ok;

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     if (!bad) {
         off = a.kv_offset[seq];
         const int slen = a.seq_lens[seq];
-        bad = L < 1 || L > a.max_len || L > slen || off < 0 || off + slen > a.total_tokens;
+        bad = L < 1 || L > a.max_len || L > slen || off < 0 || off > a.total_tokens - slen;
     }
     if (bad) {
         if (tid == 0 && blockIdx.x == 0 && layer == 0)
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kConsumers * kWarp, 1) attend_rk_kernel(const 
     int32_t* s_ent = reinterpret_cast<int32_t*>(smem);
     for (int i = tid; i < n_cap; i += kConsumers * kWarp) s_ent[i] = set[i];
     const bool bad = seq < 0 || seq >= a.n_seq || L < 1 || L > a.max_len || L > slen || off < 0 ||
-                     off + slen > a.total_tokens;
+                     off > a.total_tokens - slen;
     if (bad) {
         if (tid == 0 && blockIdx.x == 0 && layer == 0)
             flag(a.dev_status, seq < 0 || seq >= a.n_seq ? LSA_DEV_BAD_SEQ : LSA_DEV_BAD_LENGTH);
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kConsumers * kWarp, 1) attend_group_kernel(con
     const int slen = a.seq_lens[seq_c];
     pdl_enter();
     const bool bad = seq < 0 || seq >= a.n_seq || L < 1 || L > a.max_len || L > slen || off < 0 ||
-                     off + slen > a.total_tokens;
+                     off > a.total_tokens - slen;
     if (bad && split == 0 && hgrp == 0 && key % hpc == 0 && layer == 0 && lane == 0 && ph == 0)
         flag(a.dev_status, seq < 0 || seq >= a.n_seq ? LSA_DEV_BAD_SEQ : LSA_DEV_BAD_LENGTH);
     if (bad && split == 0 && ph == 0) {  // an invalid row's output is zero
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kConsumers * kWarp, 1) attend_group_kernel(con
         const int64_t o2 = a.kv_offset[sc];
         const int sl = a.seq_lens[sc];
         const bool ok = sq >= 0 && sq < a.n_seq && Lr >= 1 && Lr <= a.max_len && Lr <= sl && o2 >= 0 &&
-                        o2 + sl <= a.total_tokens;
+                        o2 <= a.total_tokens - sl;
         s_len[tid] = ok ? Lr : 0;
     }
     __syncthreads();
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kMergeMaxWarps * kWarp) attend_merge_kernel(co
             M = nm;
         }
     }
-    if (seq < 0 || seq >= a.n_seq || L < 1 || L > a.max_len || L > slen || off < 0 || off + slen > a.total_tokens)
+    if (seq < 0 || seq >= a.n_seq || L < 1 || L > a.max_len || L > slen || off < 0 || off > a.total_tokens - slen)
         return;
     const float inv = den > 0.f ? 1.f / den : 0.f;
     reinterpret_cast<float4*>(a.out[layer] + ((int64_t)r * a.H_q + h) * kD)[lane] =

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
     const int64_t off = b.kv_offset[seq_c];
     const int slen = b.seq_lens[seq_c];
     const bool bad = seq < 0 || seq >= b.n_seq || L < 1 || L > b.max_len || L > slen || off < 0 ||
-                     off + slen > b.total_tokens;
+                     off > b.total_tokens - slen;
     pdl_enter();
 
     // a team of HPC warps, one per kv head, works on every n_sel-th step of 32 entries;

@@ -219,7 +219,7 @@ __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int b) {
     s.off = a.kv_offset[b];
     s.n = end - s.row0;
     s.base = len - s.n;
-    s.ok = s.row0 >= 0 && end <= a.n_rows && s.n <= len && len <= a.max_len && s.off >= 0 && s.off + len <= a.total_tokens;
+    s.ok = s.row0 >= 0 && end <= a.n_rows && s.n <= len && len <= a.max_len && s.off >= 0 && s.off <= a.total_tokens - len;
     return s;
 }
 

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
             look_up();
         }
         if (n <= 0) continue;
-        if (row0 < 0 || (int64_t)row0 + n > a.n_rows || n > len || len > a.max_len || off < 0 || off + len > a.total_tokens) {
+        if (row0 < 0 || (int64_t)row0 + n > a.n_rows || n > len || len > a.max_len || off < 0 || off > a.total_tokens - len) {
             if (tid == 0 && part == 0 && kvh == 0 && c0 == 0) flag(a.dev_status, LSA_DEV_BAD_LENGTH);
             continue;
         }

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) attend_window_kernel(const __g
         if (r < a.n_q) {
             const int Lr = a.q_len[r];
             const bool ok = a.q_seq[r] == 0 && Lr >= 1 && Lr <= a.max_len && Lr <= slen && off >= 0 &&
-                            off + slen <= a.total_tokens;
+                            off <= a.total_tokens - slen;
             L = ok ? Lr : 0;  // an invalid row attends nothing here (the gather kernel zeroed and flagged it)
         }
         const int s = min(a.si_sink, L);

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kTkThreads, 2) topk_pairs_kernel(const __grid_
     int32_t* out = a.index_sets + (int64_t)r * a.budget;
     int32_t bits = 0;
     if (seq_q < 0 || seq_q >= a.n_seq) bits = LSA_DEV_BAD_SEQ;
-    else if (Lq < 1 || Lq > a.max_len || Lq > slen_q || off_q < 0 || off_q + slen_q > a.total_tokens)
+    else if (Lq < 1 || Lq > a.max_len || Lq > slen_q || off_q < 0 || off_q > a.total_tokens - slen_q)
         bits = LSA_DEV_BAD_LENGTH;
     if (bits != 0) {
         if (tid == 0) flag(a.dev_status, bits);

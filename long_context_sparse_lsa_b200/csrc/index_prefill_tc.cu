@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fine_score_tc_kernel(const __gr
         if (r < a.n_q) {
             const int L = a.q_len[r];
             ok = a.q_seq[r] == 0 && L >= 1 && L <= a.max_len && L <= slen && off >= 0 &&
-                 off + slen <= a.total_tokens;
+                 off <= a.total_tokens - slen;
             s = min(a.sink, L);
             ws = max(s, L - a.window);
         }

@@ -32,10 +32,10 @@ __device__ __forceinline__ bool row_ok(const IndexArgs& a, int r, int64_t& off, 
     if (seq < 0 || seq >= a.n_seq) return false;
     off = a.kv_offset[seq];
     slen = a.seq_lens[seq];
-    if (L < 1 || L > a.max_len || L > slen || off < 0 || off + slen > a.total_tokens) return false;
+    if (L < 1 || L > a.max_len || L > slen || off < 0 || off > a.total_tokens - slen) return false;
     if (a.hi_block > 0) {
         const int64_t bo = a.blk_offset[seq];
-        if (bo < 0 || bo + (L + a.hi_block - 1) / a.hi_block > a.block_rows) return false;
+        if (bo < 0 || bo > a.block_rows - (L + a.hi_block - 1) / a.hi_block) return false;
     }
     return true;
 }

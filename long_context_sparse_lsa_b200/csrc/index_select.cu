@@ -787,8 +787,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     // before the first cluster barrier
     int32_t bits = 0;
     if (seq_q < 0 || seq_q >= a.n_seq) bits = LSA_DEV_BAD_SEQ;
-    else if (Lq < 1 || Lq > a.max_len || Lq > slen_q || off_q < 0 || off_q + slen_q > a.total_tokens ||
-             (a.hi_block > 0 && (boff_q < 0 || boff_q + (Lq + a.hi_block - 1) / a.hi_block > a.block_rows)))
+    else if (Lq < 1 || Lq > a.max_len || Lq > slen_q || off_q < 0 || off_q > a.total_tokens - slen_q ||
+             (a.hi_block > 0 && (boff_q < 0 || boff_q > a.block_rows - (Lq + a.hi_block - 1) / a.hi_block)))
         bits = LSA_DEV_BAD_LENGTH;
     if constexpr (!kTokens && D_I > 0) {
         // a valid row that sees fewer tokens than its sequence holds: the

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kStThreads) store_fp4_kernel(const __grid_cons
             int64_t dst = -1;
             if (r >= lo && r < hi) {
                 if (hi <= a.n_rows && lo >= 0 && hi - lo <= len && len <= a.max_len && off >= 0 &&
-                    off + len <= a.total_tokens)
+                    off <= a.total_tokens - len)
                     dst = off + len - (hi - r);
                 else
                     flag(a.dev_status, LSA_DEV_BAD_LENGTH);
