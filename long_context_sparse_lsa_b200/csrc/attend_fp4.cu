@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(f4_warps(NT) * kWarp, 1) attend_fp4_kernel(con
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // exponent of the row's largest magnitude (0 for a row that is zero or
-        // subnormal). Every score of a row that is not finite is an infinity or
-        // NaN, and so its softmax NaN: its scale is set to NaN below
-        int e = (int)(top >> 7) - 127;
-        if (e < -126 || e > 127) e = 0;
+        // exponent of the row's largest magnitude (-126 for a row that is zero or
+        // subnormal: its numbers are multiples of 2^-133, and so whole in fp16).
+        // Every score of a row that is not finite is an infinity or NaN, and so
+        // its softmax NaN: its scale is set to NaN below
+        int e = max((int)(top >> 7) - 127, -126);
+        if (e > 127) e = 0;
         const float down = e >= 0 ? __uint_as_float((uint32_t)(127 - min(e, 126)) << 23) : __uint_as_float((uint32_t)(127 - e) << 23);
         // (the sign of the layer's scale goes with it, so that the softmax scale is not negative)
         const float rest = copysignf(e == 127 ? 0.5f : 1.f, b.kscale[layer]);

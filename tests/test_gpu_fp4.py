@@ -445,3 +445,15 @@ def test_store_flags_sequences_outside_the_rows(ro, here):
         n = ro[b + 1] - ro[b]
         want[ko[b] + lens[b] - n:ko[b] + lens[b]] = codes[ro[b]:ro[b + 1]]
     assert np.array_equal(k[0].cpu().numpy(), want) and np.array_equal(v[0].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("H,K", [(8, 1), (16, 1), (8, 4)])
+def test_attend_small_queries(H, K):
+    """Query rows around and below the smallest normal bf16, of full weight where the layer's scale is large."""
+    c = Case(H, K, 1, [300], _sets([300] * 4, 200), [0] * 4, [300] * 4, seed=H)
+    for r, e in enumerate((-124, -127, -130, -133)):
+        c.q[0][r] = (c.q[0][r].double() * 2.0 ** e).to(torch.bfloat16)
+    c.k_scale = [2.0 ** 120]  # (numbers of size 2^126: scores of size 4 to 2^-7)
+    c.run()
+    assert c.status.item() == 0 and c.q[0][2].abs().max() > 0
+    c.check()
