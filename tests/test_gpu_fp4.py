@@ -457,3 +457,19 @@ def test_attend_small_queries(H, K):
     c.run()
     assert c.status.item() == 0 and c.q[0][2].abs().max() > 0
     c.check()
+
+
+@pytest.mark.parametrize("H,pad", [(2, 8), (3, 40), (1, 136)])
+def test_store_rows_apart_by_any_multiple_of_eight(H, pad):
+    n = 77
+    x = _rand((n, H, 128), pad)
+    wide = torch.full((n * (H * 128 + pad) + 8,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y = wide.as_strided(x.shape, (H * 128 + pad, 128, 1), 8)
+    y.copy_(x)
+    assert y.data_ptr() % 32 == 16
+    k, kg, v, vg = _caches(n, H, 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lsa.lsa_store_fp4([y], [x], k, kg, v, vg, [0.5], [0.5], _prompts([n], [n], n), dev_status=status)
+    wc, wg, _ = fp4.quantise(x, 0.5)
+    assert status.item() == 0 and np.array_equal(k[0].cpu().numpy(), wc) and np.array_equal(kg[0].cpu().numpy(), wg)
+    assert torch.equal(k[0], v[0]) and torch.equal(kg[0], vg[0])

@@ -462,3 +462,18 @@ def test_log_sum_exp_of_large_scores(rows, lens, rising):
         got = c.lse[c.ro[b]:c.ro[b] + n].double()
         assert float(lse.abs().max()) > 80  # (the case is what it says)
         assert ((got - lse).abs() <= LSE + (2.0 ** -15 + 2.0 ** -21) * S).all(), (b, float(((got - lse).abs() / S).max()))
+
+
+@pytest.mark.parametrize("rows,lens", [([70, 300, 1], [70, 300, 1]), ([1, 2, 1], [700, 90, 3]), ([200], [3000]), ([17] * 3, [500, 17, 90])])
+@pytest.mark.parametrize("H,K,pad", [(8, 2, 8), (6, 2, 24), (4, 4, 136), (1, 1, 8)])
+def test_rows_apart_by_any_multiple_of_eight(rows, lens, H, K, pad):
+    """Row strides that are no whole number of heads, bases that are 16-byte aligned and no more."""
+    c = Case(H, K, rows, lens, seed=pad)
+    for name in ("q", "k", "v"):
+        x = getattr(c, name)
+        wide = torch.full((x.shape[0] * (x.shape[1] * 128 + pad) + 8,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        y = wide[8:].as_strided(x.shape, (x.shape[1] * 128 + pad, 128, 1), 8)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        setattr(c, name, y)
+    c.run().check()
