@@ -131,7 +131,9 @@ typedef struct {
 typedef struct {
     int32_t n_seq;            /* number of sequences, >= 1 */
     int32_t n_rows;           /* rows in all (bounds every row access), >= 0 */
-    int32_t max_len;          /* host-side upper bound on every seq_lens */
+    int32_t max_len;          /* host-side upper bound on every seq_lens; lsa_attend_prompt
+                                 splits the keys by it, so that a bound far above the
+                                 lengths leaves few CTAs to each sequence */
     int32_t reserved;         /* must be 0 */
     int64_t total_tokens;     /* rows in the packed caches (bounds every access) */
     const int32_t *row_offset;/* device [n_seq + 1]: first row of each sequence,
@@ -529,7 +531,7 @@ lsa_status_t lsa_attend_si(const uint16_t *const *q, const uint16_t *const *k_ca
  * over the tokens j that the row sees; scale and GQA mapping as fixed at the
  * top of this file. Sums and softmax statistics are fp32; the weights are
  * rounded to bf16 for the product with V, and the output to bf16 (it feeds
- * the output projection). A token that a row does not see never counts,
+ * the output projection): 2^-8 of the largest |v| each at most. A token that a row does not see never counts,
  * whatever its K and V hold; one that it sees and that is not finite does.
  *
  * q        device bf16 [n_rows] rows of H_q * d elements, q_stride elements
@@ -545,7 +547,10 @@ lsa_status_t lsa_attend_si(const uint16_t *const *q, const uint16_t *const *k_ca
  *          needed; may be NULL when that is 0).
  * All device pointers 16-byte aligned (out 32, lse 4). Supported: d == 128; H_q / H_kv
  * a whole number up to 64; H_q <= 4096; n_rows * H_q < 2^31. One launch, plus
- * a merge where the workspace size is not 0.
+ * a merge where the workspace size is not 0. Whether a batch is taken as one of
+ * a token or two per sequence goes by n_rows / n_seq; longer chunks among them
+ * are taken there too, at the cost of reading K and V once per 8 or 16 (row,
+ * query head) pairs of a kv head.
  */
 size_t lsa_attend_prompt_workspace_size(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
 int32_t lsa_attend_prompt_launches(const lsa_prompts_t *prompts, int32_t H_q, int32_t H_kv, int32_t d);
