@@ -1072,6 +1072,7 @@ lsa_status_t lsa_attend_prompt(const uint16_t* q, int64_t q_stride, const uint16
     a.n_parts = p.n_parts;
     a.part_keys = p.part_keys;
     a.helpers = p.helpers;
+    a.further = p.further;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
     cudaError_t e = lsa::launch_attend_prompt(a, p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LSA_OK : cuda_fail(e);

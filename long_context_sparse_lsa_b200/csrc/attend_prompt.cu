@@ -800,9 +800,9 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
         if (p.part_keys < 128) p.part_keys = 128;
         p.n_parts = (int)(((int64_t)max_len + p.part_keys - 1) / p.part_keys);
         // further runs of columns: all there could be (if one sequence had all rows), or as many as run at once
-        const int64_t runs = ((int64_t)n_rows * p.G - 1) / few_columns(n_seq, n_rows, p.G);
+        p.further = (int)(((int64_t)n_rows * p.G - 1) / few_columns(n_seq, n_rows, p.G));
         const int64_t at_a_time = 2 * num_sms / ((int64_t)p.n_parts * H_kv);
-        p.helpers = (int)(runs < at_a_time || runs == 0 ? runs : at_a_time > 1 ? at_a_time : 1);
+        p.helpers = p.further < at_a_time || p.further == 0 ? p.further : at_a_time > 1 ? (int)at_a_time : 1;
         if (p.n_parts > kFewJoined || !at_once(p.n_parts)) workspace();
         return p;
     }

@@ -61,9 +61,9 @@ __device__ __forceinline__ uint32_t fw_at(int m, int c) { return (uint32_t)(m * 
 template <int W, int kEach>
 __device__ __forceinline__ bool find_columns(const PromptArgs& a, int i, int& seq, int& c0) {
     const int lane = lane_id();
-    auto runs = [&](int b) {
-        const int n = min(a.row_offset[min(b + 1, a.n_seq)] - a.row_offset[min(b, a.n_seq)], a.n_rows);
-        return n > 0 ? (n * a.G - 1) / W : 0;
+    auto runs = [&](int b) {  // (of a sequence that lies outside the rows: none)
+        const int start = a.row_offset[min(b, a.n_seq)], end = a.row_offset[min(b + 1, a.n_seq)];
+        return start >= 0 && end <= a.n_rows && end > start ? ((end - start) * a.G - 1) / W : 0;
     };
     for (int b0 = 0; b0 < a.n_seq; b0 += kEach * kWarp) {
         int mine = 0;
@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
     bool found = helper < 0 || further_columns<8 * NT>(a, helper, seq, c0);
     if (found) look_up();
     pdl_enter();
-    for (int turn = helper; found; found = helper >= 0 && further_columns<8 * NT>(a, turn += a.helpers, seq, c0)) {
+    // (offsets that ascend have no more runs than `further`; others end the helpers' turns there)
+    auto next = [&](int& turn) { return helper >= 0 && (turn += a.helpers) < a.further && further_columns<8 * NT>(a, turn, seq, c0); };
+    for (int turn = helper; found; found = next(turn)) {
         if (turn != helper) {
             __syncthreads();  // the merge area of the columns before
             look_up();

@@ -282,12 +282,12 @@ struct PromptArgs {
     int32_t n_splits;                  // key splits of each row tile
     int32_t dual, n_parts;             // a CTA's two tiles are of the same rows; partials per row
     int32_t part_keys;                 // few rows: keys of a part (else 0)
-    int32_t helpers;                   // few rows: grid rows for further columns of any sequence
+    int32_t helpers, further;          // few rows: grid rows for further runs of columns, and such runs at most
     float scale_log2;
 };
 struct PromptPlan {
     int G = 1, tile_tokens = 128, n_splits = 1, n_parts = 1;
-    int part_keys = 0, helpers = 0;
+    int part_keys = 0, helpers = 0, further = 0;
     bool few = false, dual = false;
     int64_t n_items = 0;
     size_t off_ml = 0, ws_bytes = 0;

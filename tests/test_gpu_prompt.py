@@ -477,3 +477,21 @@ def test_rows_apart_by_any_multiple_of_eight(rows, lens, H, K, pad):
         assert y.data_ptr() % 32 == 16
         setattr(c, name, y)
     c.run().check()
+
+
+@pytest.mark.parametrize("n_seq,G", [(40, 8), (4000, 2)])
+def test_row_offsets_that_do_not_ascend_end(n_seq, G):
+    """Offsets that go up and down name the same rows over and over: the call ends after no more runs of columns than the
+    rows can hold. Ones that ascend far behind the rows have no runs."""
+    n = 2 * n_seq * 8 // G  # rows that still count as a few per sequence
+    c = Case(G, 1, [n] + [0] * (n_seq - 1), [n] + [1] * (n_seq - 1), seed=1)
+    c.pr.row_offset.copy_(torch.tensor([0, n] * n_seq, dtype=torch.int32, device=DEV)[:n_seq + 1])
+    c.pr.kv_offset.zero_()
+    c.pr.seq_lens.fill_(n)
+    c.run()
+    torch.cuda.synchronize()
+    up = torch.arange(n_seq, device=DEV) * (1 << 16)  # ascending, far behind the rows
+    c.pr.row_offset[1:] = up.to(torch.int32) + n + 1
+    c.out.fill_(9.0)
+    c.run()
+    assert c.status.item() & lsa.LSA_DEV_BAD_LENGTH and (c.out == 9).all()
