@@ -39,10 +39,11 @@
 //  * Partials of split keys are combined by prompt_merge_kernel by log-sum-exp.
 //  * What bounds it: the chain of one row tile, softmax (1950 cycles), P V (512),
 //    the next S (512) and their hand-overs (350), whose tensor part the other row
-//    tile's fills to 61%; with long prompts the board's power as well (1.6 to
-//    1.7 GHz): 16384 tokens, 32/4 heads, 1140 TFLOP/s. Short prompts (24 of up to
-//    1500 tokens: 640 TFLOP/s) add 8000 cycles an item for the first S, the
-//    masked tile and the output.
+//    tile's fills to 62%; with long prompts the board's power as well: 16384
+//    tokens, 32/4 heads, 1702 us (1292 TFLOP/s) in the first milliseconds, 1969
+//    (1117 TFLOP/s) at the 1.52 GHz that a loop of it holds under the 1000 W cap.
+//    Short prompts (24 of up to 1500 tokens: 624 TFLOP/s, tensor pipe 40%) add
+//    8000 cycles an item for the first S, the masked tile and the output.
 //  * Every wait is bounded; on expiry the kernel flags LSA_DEV_TIMEOUT, waits
 //    (bounded) for what it issued, frees its tensor memory and returns.
 #include "internal.h"
