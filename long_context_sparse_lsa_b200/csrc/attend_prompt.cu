@@ -790,7 +790,7 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
     // 16.7 us; 9 over up to 1000, eight parts on 97% of the places, 9.8 and 8.2),
     // and parts of up to 256 keys are taken for that (4 over up to 2000: 7.0
     // against 8.6 us).
-    p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65000;
+    p.few = (int64_t)n_rows * p.G <= 16 * (int64_t)n_seq && n_seq <= 65534;
     if (p.few) {
         const int64_t units = (int64_t)n_seq * H_kv;
         int64_t parts = (2 * (int64_t)num_sms + units - 1) / units;
@@ -804,6 +804,7 @@ PromptPlan plan_prompt(int n_seq, int n_rows, int max_len, int H_q, int H_kv, in
         p.further = (int)(((int64_t)n_rows * p.G - 1) / few_columns(n_seq, n_rows, p.G));
         const int64_t at_a_time = 2 * num_sms / ((int64_t)p.n_parts * H_kv);
         p.helpers = p.further < at_a_time || p.further == 0 ? p.further : at_a_time > 1 ? (int)at_a_time : 1;
+        if (p.helpers > 65535 - n_seq) p.helpers = 65535 - n_seq;  // (the grid's third axis holds them behind the sequences)
         if (p.n_parts > kFewJoined || !at_once(p.n_parts)) workspace();
         return p;
     }

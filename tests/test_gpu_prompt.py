@@ -495,3 +495,10 @@ def test_row_offsets_that_do_not_ascend_end(n_seq, G):
     c.out.fill_(9.0)
     c.run()
     assert c.status.item() & lsa.LSA_DEV_BAD_LENGTH and (c.out == 9).all()
+
+
+@pytest.mark.parametrize("n", [65533, 65534, 65535])
+def test_sequences_up_to_the_end_of_a_grid_axis(n):
+    """Single tokens and, last, a sequence of 70."""
+    c = Case(2, 1, [1] * (n - 1) + [70], [1 + i % 3 for i in range(n - 1)] + [90], seed=4).run()
+    c.check(skip=set(range(n)) - set(range(0, n, n // 20)) - {n - 1})
