@@ -532,7 +532,8 @@ lsa_status_t lsa_attend_si(const uint16_t *const *q, const uint16_t *const *k_ca
  * top of this file. Sums and softmax statistics are fp32; the weights are
  * rounded to bf16 for the product with V, and the output to bf16 (it feeds
  * the output projection): 2^-8 of the largest |v| each at most. A token that a row does not see never counts,
- * whatever its K and V hold; one that it sees and that is not finite does.
+ * whatever its K and V hold; one that it sees and that is not finite does. A
+ * row and head with a score of NaN or +infinity is NaN, its lse too.
  *
  * q        device bf16 [n_rows] rows of H_q * d elements, q_stride elements
  *          from one row to the next.

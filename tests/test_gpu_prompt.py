@@ -502,3 +502,26 @@ def test_sequences_up_to_the_end_of_a_grid_axis(n):
     """Single tokens and, last, a sequence of 70."""
     c = Case(2, 1, [1] * (n - 1) + [70], [1 + i % 3 for i in range(n - 1)] + [90], seed=4).run()
     c.check(skip=set(range(n)) - set(range(0, n, n // 20)) - {n - 1})
+
+
+@pytest.mark.parametrize("rows,lens", [([40], [300]), ([1, 1], [3000, 50]), ([2, 1], [200, 300]), ([100], [4000])])
+@pytest.mark.parametrize("x", [float("inf"), float("-inf")])
+def test_infinite_scores(rows, lens, x):
+    """A score of +infinity makes its row and head NaN, the log-sum-exp as well; one of -infinity has no weight."""
+    c = Case(8, 2, rows, lens, seed=13)
+    at = lens[0] - rows[0]  # seen by every row of the first sequence
+    c.k[c.ko[0] + at, 0, 7] = x
+    c.run()
+    assert c.status.item() == 0
+    up = c.q[:rows[0], :4, 7].double() * x > 0  # of the heads that read kv head 0
+    out, lse = c.out[:rows[0], :4], c.lse[:rows[0], :4]
+    assert torch.equal(out.isnan().any(-1), up) and torch.equal(out.isnan().all(-1), up) and torch.equal(lse.isnan(), up)
+    q, k, v = c.q[:rows[0]].double(), c.k[c.ko[0]:c.ko[0] + lens[0]].double(), c.v[c.ko[0]:c.ko[0] + lens[0]].double()
+    z = torch.einsum("rhd,td->hrt", q[:, :4], k[:, 0]) / 128 ** 0.5
+    z[:, :, at] = -torch.inf  # (the rows whose score is +infinity are not compared)
+    z.masked_fill_(torch.arange(lens[0], device=DEV) > torch.arange(lens[0] - rows[0], lens[0], device=DEV)[:, None], -torch.inf)
+    p = torch.softmax(z, -1)
+    want = torch.einsum("hrt,td->rhd", p, v[:, 0])
+    fine = ~up
+    assert ((out.double() - want)[fine].abs() <= MAX * v.abs().max()).all()
+    assert ((lse.double() - torch.logsumexp(z, -1).T)[fine].abs() <= LSE).all()
