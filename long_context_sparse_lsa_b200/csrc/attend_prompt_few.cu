@@ -19,7 +19,8 @@
 // part has a fixed number of keys, so that CTAs are alike whatever the
 // sequences' lengths; those behind a sequence's end have nothing to do. In a
 // cluster it is an equal share of its sequence.
-//  * Whether a batch comes here goes by its mean of rows, so single sequences
+//
+// Whether a batch comes here goes by its mean of rows, so single sequences
 // may have many more columns than the 8 or 16 that a CTA takes. Such further
 // runs of columns are other CTAs' work: about as many as run at once, behind
 // the sequences' own in the grid, take them in turn (one chunk of 64 rows on
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kFwThreads, 2) attend_prompt_few_kernel(const 
         auto fetch = [&](int i, int slot) {
             if (i < n_tiles) {
                 const uint32_t to = ring + (uint32_t)(slot * kFwTileBytes);
-    #pragma unroll
+#pragma unroll
                 for (int x = 0; x < kFwTile / 2; ++x) {
                     const int m = 2 * x + (lane >> 4);
                     const int key = k_lo + i * kFwTile + m;
